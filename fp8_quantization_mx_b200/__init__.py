@@ -24,6 +24,10 @@ Two layers, both exported here:
 * ``MXFakeQuantize``: an autograd function (forward fake-quant, straight-
   through backward) for quantization-aware training of activations and
   weights alike.
+* ``quantize128``, ``rms_norm_quantize``, ``rms_norm_bwd``, ``gemm128`` (and
+  the C functions under them): FP8 with one float32 scale per 128 elements,
+  the operators of a linear layer's forward and backward pass;
+  ``linear128`` and ``rms_norm_linear128`` are both passes with autograd.
 """
 
 from __future__ import annotations
@@ -43,6 +47,9 @@ __all__ = [
     "mx_bat_apply", "mx_bat_quantize", "bat_apply", "bat_quantize",
     "mx_gemm", "mx_quant_gemm", "gemm", "quant_gemm", "GEMM_A_ON_CHIP", "mx_quant_gemm_noalloc",
     "MXFP4_FORMAT", "MXFP8_FORMAT",
+    "BLOCK128", "POW2_SCALES", "mx_quantize128", "mx_rms_norm_quant128", "mx_rms_norm_bwd",
+    "mx_rms_norm_bwd_workspace", "mx_gemm128", "quantize128", "rms_norm_quantize", "rms_norm_bwd",
+    "gemm128", "FP8Linear128", "FP8NormLinear128", "linear128", "rms_norm_linear128",
 ]
 
 # formats (mx_format_t)
@@ -57,6 +64,9 @@ INT8 = 5   # MXINT8 (i * 2^-6)
 MMA_SCALES = 1 << 8
 # OR into mx_quant_gemm's out_fp32: A quantized in the GEMM's prologue, on chip
 GEMM_A_ON_CHIP = 1 << 9
+# flags of the operators with float32 scales per 128 elements
+BLOCK128 = 1 << 10
+POW2_SCALES = 1 << 11
 E2M1_B16 = 6  # MXFP4 at block 16 (E8M0 scales [..., cols/16])
 NVFP4 = 7     # E2M1 at block 16 with E4M3 scales amax/6 (FLOOR only)
 _PACKED = (E2M1, E2M1_B16, NVFP4)
@@ -121,6 +131,18 @@ def load_library():
     lib.mx_quant_gemm.restype = c_int
     lib.mx_quant_gemm_noalloc.argtypes = [vp, c_int, vp, vp, i64, i64, i64, c_int, vp, vp, vp]
     lib.mx_quant_gemm_noalloc.restype = c_int
+    f32 = ctypes.c_float
+    lib.mx_quantize128.argtypes = [vp, c_int, i64, i64, i64, c_int, c_int, vp, i64, vp, i64, vp, i64,
+                                   vp, i64, vp]
+    lib.mx_rms_norm_quant128.argtypes = [vp, i64, vp, vp, c_int, i64, i64, f32, c_int, c_int, vp, vp,
+                                         vp, i64, vp, i64, vp]
+    lib.mx_rms_norm_bwd_workspace.argtypes = [i64, i64]
+    lib.mx_rms_norm_bwd_workspace.restype = i64
+    lib.mx_rms_norm_bwd.argtypes = [vp, vp, vp, vp, c_int, i64, i64, f32, vp, vp, vp, vp]
+    lib.mx_gemm128.argtypes = [vp, i64, vp, i64, c_int, vp, i64, vp, i64, c_int, c_int, i64, i64, i64,
+                               c_int, vp, vp, vp]
+    for f in ("mx_quantize128", "mx_rms_norm_quant128", "mx_rms_norm_bwd", "mx_gemm128"):
+        getattr(lib, f).restype = c_int
     _lib = lib
     return lib
 
@@ -176,6 +198,35 @@ def mx_quant_gemm_noalloc(a, scaling, b_codes, b_scales, M, N, K, out_fp32, d, s
     while they run. Calls that overlap on the GPU race on that array."""
     return load_library().mx_quant_gemm_noalloc(a, scaling, b_codes, b_scales, M, N, K, out_fp32,
                                                 d, status, stream)
+
+
+def mx_quantize128(x, dtype, rows, cols, ldx, format, flags, codes, ldc, scales, lds, codes_t, ldct,
+                   scales_t, ldst, stream=0) -> int:
+    return load_library().mx_quantize128(x, dtype, rows, cols, ldx, format, flags, codes, ldc, scales,
+                                         lds, codes_t, ldct, scales_t, ldst, stream)
+
+
+def mx_rms_norm_quant128(x, ldx, residual, weight, dtype, rows, cols, eps, format, flags, h_out,
+                         y_out, codes, ldc, scales, lds, stream=0) -> int:
+    return load_library().mx_rms_norm_quant128(x, ldx, residual, weight, dtype, rows, cols, eps,
+                                               format, flags, h_out, y_out, codes, ldc, scales, lds,
+                                               stream)
+
+
+def mx_rms_norm_bwd_workspace(rows, cols) -> int:
+    return load_library().mx_rms_norm_bwd_workspace(rows, cols)
+
+
+def mx_rms_norm_bwd(grad_y, h, weight, grad_residual, dtype, rows, cols, eps, grad_h, grad_weight,
+                    workspace, stream=0) -> int:
+    return load_library().mx_rms_norm_bwd(grad_y, h, weight, grad_residual, dtype, rows, cols, eps,
+                                          grad_h, grad_weight, workspace, stream)
+
+
+def mx_gemm128(a_codes, lda, a_scales, ldsa, a_format, b_codes, ldb, b_scales, ldsb, b_format,
+               b_flags, M, N, K, out_fp32, d, status, stream=0) -> int:
+    return load_library().mx_gemm128(a_codes, lda, a_scales, ldsa, a_format, b_codes, ldb, b_scales,
+                                     ldsb, b_format, b_flags, M, N, K, out_fp32, d, status, stream)
 
 
 def mx_status_string(status: int) -> str:
@@ -631,3 +682,10 @@ def quant_gemm(a: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
                              _ptr(d), _ptr(ac), _ptr(asc), _ptr(st), _stream(dev)),
                "mx_quant_gemm")
     return d
+
+
+# ------------------------------------- FP8 with scales per 128 elements --
+# (its tensor layer is a module of its own, built on the C layer above)
+
+from .ops128 import (FP8Linear128, FP8NormLinear128, gemm128, linear128, quantize128,  # noqa: E402
+                     rms_norm_bwd, rms_norm_linear128, rms_norm_quantize)

@@ -91,7 +91,9 @@ const char* mx_status_string(int status) {
   switch (status) {
     case MX_OK: return "ok";
     case MX_ERR_INVALID_ARG: return "invalid argument (null pointer or bad shape)";
-    case MX_ERR_SHAPE: return "cols must be a multiple of 32 (of 128 with macro block scaling)";
+    case MX_ERR_SHAPE:
+      return "cols must be a multiple of 32 (of 128 with macro block scaling); with 128-element "
+             "scales: a row pitch too small or not a multiple of 16 bytes";
     case MX_ERR_ALIGN: return "pointer is not aligned as required";
     case MX_ERR_UNSUPPORTED: return "unsupported format / scaling combination";
     case MX_ERR_CUDA: return "CUDA launch or stream operation failed";

@@ -49,4 +49,21 @@ cudaError_t launch_quant_gemm_noalloc(const void* a, int a_rule, const void* b_c
 cudaError_t launch_block_error(const void* x, int64_t n, int fmt, int scaling, float* block_sse,
                                double* totals, cudaStream_t st);
 
+// FP8 with float scales per 128 elements (mx_quant128.cu, mx_norm128.cu; the
+// GEMM is mx_gemm128.h). dtype: 0 bf16, 1 fp16, 2 float. A null codes /
+// codes_t leaves that direction out.
+cudaError_t launch_quant128(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            bool e5m2, bool block, bool pow2, uint8_t* codes, int64_t ldc,
+                            float* scales, int64_t lds, uint8_t* codes_t, int64_t ldct,
+                            float* scales_t, int64_t ldst, cudaStream_t st);
+cudaError_t launch_norm128(const void* x, int64_t ldx, const void* residual, const void* weight,
+                           int dtype, int64_t rows, int64_t cols, float eps, bool e5m2, bool pow2,
+                           void* h, void* y, uint8_t* codes, int64_t ldc, float* scales,
+                           int64_t lds, cudaStream_t st);
+// part: kNormParts * cols floats at most (min(rows, kNormParts) * cols).
+constexpr int kNormParts = 592;
+cudaError_t launch_norm_bwd(const void* gy, const void* h, const void* weight, const void* gres,
+                            int dtype, int64_t rows, int64_t cols, float eps, void* gh, float* gw,
+                            float* part, cudaStream_t st);
+
 }  // namespace mxk

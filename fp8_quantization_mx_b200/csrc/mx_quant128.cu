@@ -1,0 +1,291 @@
+// FP8 quantization with float scales per 1 x 128 tile or 128 x 128 block,
+// along the rows, along the columns (codes of the transposed matrix), or both
+// from one read of x.
+//
+// One CTA of 256 threads takes a 128 x 128 piece of x: thread t holds rows
+// 4 (t / 8) .. + 3, columns 16 (t % 8) .. + 15, in registers.
+//   rows     a tile is 8 neighbouring lanes: three shuffles give its largest
+//            magnitude, 16 codes are one 16-byte store, and a lane group's four
+//            scales one 16-byte store of the block-major scale array
+//   columns  the largest magnitudes of a column over the four rows of a
+//            thread, over the warp's four lane groups (an exchange that halves
+//            the columns held at each step: 12 shuffles where reducing all 16
+//            in every lane takes 32) and, through shared memory, over the eight
+//            warps; the four codes of a column are one word, transposed through
+//            shared memory (words permuted so that both sides are free of bank
+//            conflicts) into 128-byte runs of the transposed codes
+//   block    one scale for the piece; its codes are made once, and the
+//            transposed codes by byte permutes of four rows' words
+// Bound by HBM: x is read once and every code written once.
+
+#include <cuda_runtime.h>
+
+#include "mx_launch.h"
+#include "mx_tile128.cuh"
+
+namespace mxk {
+
+namespace {
+
+using namespace t128;
+
+struct Quant128Args {
+  const void* x;
+  int64_t rows, cols, ldx;
+  uint8_t* codes;     // [rows, ldc]
+  int64_t ldc;
+  float* scales;      // tiles: [ceil(cols/128), lds]; blocks: [ceil(rows/128), ceil(cols/128)]
+  int64_t lds;
+  uint8_t* codes_t;   // [cols, ldct]
+  int64_t ldct;
+  float* scales_t;    // tiles: [ceil(rows/128), ldst]; blocks: [ceil(cols/128), ceil(rows/128)]
+  int64_t ldst;
+  int64_t nbr, nbc;   // pieces along the rows and the columns
+  int pow2;
+  int vec;            // x and ldx allow 16-byte loads
+};
+
+constexpr int kThreads = 256;
+
+// The word of codes of column c (0..127), rows 4g .. 4g + 3, in the transposed
+// piece: 32 words a column, permuted by the column's group of 16 so that the
+// eight lanes that write a column of their own group hit eight bank quads.
+__device__ __forceinline__ int word_at(int c, int g) { return c * 32 + (g ^ (((c >> 4) & 7) << 2)); }
+
+template <bool E5M2, bool SLOW, int DT>
+__device__ __forceinline__ uint4 encode_row(const Vec<DT, 16>& v, float s, float inv) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = enc4<E5M2>(div_scale<SLOW>(v.get(4 * i), s, inv), div_scale<SLOW>(v.get(4 * i + 1), s, inv),
+                      div_scale<SLOW>(v.get(4 * i + 2), s, inv),
+                      div_scale<SLOW>(v.get(4 * i + 3), s, inv));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool E5M2, bool SLOW, int DT>
+__device__ __forceinline__ void encode_cols(const Vec<DT, 16> (&v)[4], const float* col_s,
+                                            const float* col_inv, int g, int sub, uint32_t* out) {
+#pragma unroll
+  for (int c4 = 0; c4 < 4; ++c4) {
+    const float4 s = reinterpret_cast<const float4*>(col_s)[sub * 4 + c4];
+    const float4 inv = reinterpret_cast<const float4*>(col_inv)[sub * 4 + c4];
+    const float ss[4] = {s.x, s.y, s.z, s.w}, ii[4] = {inv.x, inv.y, inv.z, inv.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = 4 * c4 + j;
+      out[word_at(sub * 16 + c, g)] = enc4<E5M2>(
+          div_scale<SLOW>(v[0].get(c), ss[j], ii[j]), div_scale<SLOW>(v[1].get(c), ss[j], ii[j]),
+          div_scale<SLOW>(v[2].get(c), ss[j], ii[j]), div_scale<SLOW>(v[3].get(c), ss[j], ii[j]));
+    }
+  }
+}
+
+template <int DT, bool E5M2, bool ROWS, bool COLS, bool BLOCK>
+__global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a) {
+  using T = typename Elem<DT>::T;
+  __shared__ __align__(16) uint32_t sh_codes[COLS ? 128 * 32 : 4];
+  __shared__ __align__(16) float sh_red[8][BLOCK ? 4 : 128];
+  __shared__ __align__(16) float sh_s[128], sh_inv[128];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = tid >> 3, sub = tid & 7;
+  const int64_t rb = blockIdx.x / a.nbc, cb = blockIdx.x % a.nbc;
+  const int64_t row0 = rb * 128 + 4 * g, col0 = cb * 128 + 16 * sub;
+
+  Vec<DT, 16> v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T* p = static_cast<const T*>(a.x) + (row0 + i) * a.ldx + col0;
+    if (row0 + i >= a.rows || col0 >= a.cols)
+      v[i].zero();
+    else if (a.vec && col0 + 16 <= a.cols)
+      v[i].load(p);
+    else
+      v[i].load_some(p, a.cols - col0);
+  }
+
+  uint4 rcodes[4];   // BLOCK: the four rows' codes
+  if constexpr (BLOCK) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m = amax2(m, v[i].get(c));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
+    if (lane == 0) sh_red[warp][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = amax2(m, sh_red[w][0]);
+    const float s = tile_scale<E5M2>(m, a.pow2);
+    const float inv = recip(s);
+    if (s < kSlowScale) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rcodes[i] = encode_row<E5M2, true, DT>(v[i], s, inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rcodes[i] = encode_row<E5M2, false, DT>(v[i], s, inv);
+    }
+    if (tid == 0) {
+      if (ROWS) a.scales[rb * a.nbc + cb] = s;
+      if (COLS) a.scales_t[cb * a.nbr + rb] = s;
+    }
+  }
+
+  if constexpr (ROWS) {
+    float s4[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 codes;
+      if constexpr (BLOCK) {
+        codes = rcodes[i];
+      } else {
+        float m = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) m = amax2(m, v[i].get(c));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
+        const float s = tile_scale<E5M2>(m, a.pow2);
+        const float inv = recip(s);
+        codes = s < kSlowScale ? encode_row<E5M2, true, DT>(v[i], s, inv)
+                               : encode_row<E5M2, false, DT>(v[i], s, inv);
+        s4[i] = s;
+      }
+      // (a row's 16-byte piece ends within the row's padding to 16 bytes)
+      if (row0 + i < a.rows && col0 < a.cols)
+        *reinterpret_cast<uint4*>(a.codes + (row0 + i) * a.ldc + col0) = codes;
+    }
+    // four rows' scales; lds >= rows rounded up to 4
+    if (!BLOCK && sub == 0 && row0 < a.rows)
+      *reinterpret_cast<float4*>(a.scales + cb * a.lds + row0) =
+          make_float4(s4[0], s4[1], s4[2], s4[3]);
+  }
+
+  if constexpr (COLS) {
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        const uint32_t* r[4] = {&rcodes[0].x, &rcodes[1].x, &rcodes[2].x, &rcodes[3].x};
+        const uint32_t ab = __byte_perm(r[0][c4], r[1][c4], 0x5140);   // a0 b0 a1 b1
+        const uint32_t AB = __byte_perm(r[0][c4], r[1][c4], 0x7362);   // a2 b2 a3 b3
+        const uint32_t cd = __byte_perm(r[2][c4], r[3][c4], 0x5140);
+        const uint32_t CD = __byte_perm(r[2][c4], r[3][c4], 0x7362);
+        const int c = sub * 16 + 4 * c4;
+        sh_codes[word_at(c, g)] = __byte_perm(ab, cd, 0x5410);
+        sh_codes[word_at(c + 1, g)] = __byte_perm(ab, cd, 0x7632);
+        sh_codes[word_at(c + 2, g)] = __byte_perm(AB, CD, 0x5410);
+        sh_codes[word_at(c + 3, g)] = __byte_perm(AB, CD, 0x7632);
+      }
+    } else {
+      float m[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        m[c] = fabsf(v[0].get(c));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m[c] = amax2(m[c], v[i].get(c));
+      }
+      // each step keeps half of the columns held: lane bit 3 columns 8-15 of
+      // the 16, then lane bit 4 the upper four of those eight
+      float h[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float keep = (lane & 8) ? m[c + 8] : m[c];
+        const float give = (lane & 8) ? m[c] : m[c + 8];
+        h[c] = amax2(keep, __shfl_xor_sync(~0u, give, 8));
+      }
+      float q[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float keep = (lane & 16) ? h[c + 4] : h[c];
+        const float give = (lane & 16) ? h[c] : h[c + 4];
+        q[c] = amax2(keep, __shfl_xor_sync(~0u, give, 16));
+      }
+      const int c0 = sub * 16 + ((lane & 8) ? 8 : 0) + ((lane & 16) ? 4 : 0);
+      *reinterpret_cast<float4*>(&sh_red[warp][c0]) = make_float4(q[0], q[1], q[2], q[3]);
+      __syncthreads();
+      if (tid < 128) {
+        float mm = sh_red[0][tid];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) mm = amax2(mm, sh_red[w][tid]);
+        const float s = tile_scale<E5M2>(mm, a.pow2);
+        sh_s[tid] = s;
+        sh_inv[tid] = recip(s);
+        // (columns past the edge: zero tiles; ldst >= cols rounded up to 4)
+        if (cb * 128 + tid < ((a.cols + 3) & ~int64_t(3))) a.scales_t[rb * a.ldst + cb * 128 + tid] = s;
+      }
+      __syncthreads();
+      bool slow = false;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) slow |= sh_s[sub * 16 + c] < kSlowScale;
+      if (slow)
+        encode_cols<E5M2, true, DT>(v, sh_s, sh_inv, g, sub, sh_codes);
+      else
+        encode_cols<E5M2, false, DT>(v, sh_s, sh_inv, g, sub, sh_codes);
+    }
+    __syncthreads();
+    // eight lanes write a column's 128 codes; 32 columns at a time
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (tid >> 3) + 32 * i, part = tid & 7;
+      const int64_t col = cb * 128 + c, row = rb * 128 + 16 * part;
+      const uint4 w = *reinterpret_cast<const uint4*>(&sh_codes[word_at(c, 4 * part)]);
+      if (col < a.cols && row < a.rows)
+        *reinterpret_cast<uint4*>(a.codes_t + col * a.ldct + row) = w;
+    }
+  }
+}
+
+template <int DT, bool E5M2>
+cudaError_t launch_fmt(const Quant128Args& a, bool block, cudaStream_t st) {
+  const int64_t pieces = a.nbr * a.nbc;
+  if (pieces > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(pieces);
+  const bool rows = a.codes != nullptr, cols = a.codes_t != nullptr;
+  if (block) {
+    if (rows && cols) quant128_kernel<DT, E5M2, true, true, true><<<grid, kThreads, 0, st>>>(a);
+    else if (rows) quant128_kernel<DT, E5M2, true, false, true><<<grid, kThreads, 0, st>>>(a);
+    else quant128_kernel<DT, E5M2, false, true, true><<<grid, kThreads, 0, st>>>(a);
+  } else {
+    if (rows && cols) quant128_kernel<DT, E5M2, true, true, false><<<grid, kThreads, 0, st>>>(a);
+    else if (rows) quant128_kernel<DT, E5M2, true, false, false><<<grid, kThreads, 0, st>>>(a);
+    else quant128_kernel<DT, E5M2, false, true, false><<<grid, kThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quant128(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            bool e5m2, bool block, bool pow2, uint8_t* codes, int64_t ldc,
+                            float* scales, int64_t lds, uint8_t* codes_t, int64_t ldct,
+                            float* scales_t, int64_t ldst, cudaStream_t st) {
+  Quant128Args a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.codes = codes;
+  a.ldc = ldc;
+  a.scales = scales;
+  a.lds = lds;
+  a.codes_t = codes_t;
+  a.ldct = ldct;
+  a.scales_t = scales_t;
+  a.ldst = ldst;
+  a.nbr = (rows + 127) / 128;
+  a.nbc = (cols + 127) / 128;
+  a.pow2 = pow2;
+  const int64_t bytes = dtype == kFP32 ? 4 : 2;
+  a.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows == 1 || ldx * bytes % 16 == 0);
+  switch (dtype * 2 + (e5m2 ? 1 : 0)) {
+    case 0: return launch_fmt<kBF16, false>(a, block, st);
+    case 1: return launch_fmt<kBF16, true>(a, block, st);
+    case 2: return launch_fmt<kFP16, false>(a, block, st);
+    case 3: return launch_fmt<kFP16, true>(a, block, st);
+    case 4: return launch_fmt<kFP32, false>(a, block, st);
+    default: return launch_fmt<kFP32, true>(a, block, st);
+  }
+}
+
+}  // namespace mxk

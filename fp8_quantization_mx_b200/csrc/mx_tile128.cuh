@@ -1,0 +1,175 @@
+// FP8 codes with one float scale per 128 elements: what the quantizer and the
+// norm share. A tile is 128 consecutive elements of a row (or of a column), a
+// block 128 x 128 of them; both may be cut short by the matrix's edge.
+//
+//   s = max(amax / maxv, 2^-126), rounded to float (maxv 448 or 57344), or
+//       the smallest power of two >= 2^-126 with amax <= maxv s;
+//   code = RNE_sat(x / s), x / s rounded to float first;
+//   NaN or Inf in the tile: s = NaN and every code NaN (0x7F).
+//
+// The floor of 2^-126 keeps s normal and nonzero, so that a zero tile needs no
+// case of its own (its codes are +-0) and 1 / s never overflows.
+
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace mxk {
+namespace t128 {
+
+constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126
+// Below this scale the remainder x - q s of div_scale may be subnormal for an
+// x that still rounds to a nonzero code; such tiles divide instead.
+constexpr float kSlowScale = 8.2718061e-25f;    // 2^-80
+
+template <bool E5M2>
+__device__ __forceinline__ constexpr float max_code() {
+  return E5M2 ? 57344.0f : 448.0f;
+}
+
+// max(|a|, |b|) that keeps a NaN (a >= 0 or NaN).
+__device__ __forceinline__ float amax2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The scale of a tile from its largest magnitude.
+template <bool E5M2>
+__device__ __forceinline__ float tile_scale(float amax, bool pow2) {
+  if (!(amax < __int_as_float(0x7f800000))) return __int_as_float(0x7fc00000);
+  if (!pow2) return fmaxf(__fdiv_rn(amax, max_code<E5M2>()), kTinyScale);
+  // maxv = 1.75 2^top: the exponent of amax less `top`, one more where the
+  // significand is above 1.75 (in biased exponents, at least 1)
+  constexpr int kTop = E5M2 ? 15 : 8;
+  const int bits = __float_as_int(amax);
+  const int e = (bits >> 23) - kTop + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  return __int_as_float((e < 1 ? 1 : e) << 23);
+}
+
+__device__ __forceinline__ float recip(float s) { return __frcp_rn(s); }
+
+// x / s correctly rounded, given inv = 1 / s correctly rounded: a quotient
+// within one unit in the last place, corrected by its exact remainder
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990). Three multiply-adds per element where a division takes
+// about ten; the rounded quotient is what ties of the codes are decided on.
+template <bool SLOW>
+__device__ __forceinline__ float div_scale(float x, float s, float inv) {
+  if constexpr (SLOW) return __fdiv_rn(x, s);
+  const float q = x * inv;
+  return fmaf(-fmaf(q, s, -x), inv, q);   // (signs chosen so that -0 / s stays -0)
+}
+
+// Two codes: lo in bits 0-7, hi in bits 8-15.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t enc2(float lo, float hi) {
+  uint16_t r;
+  if constexpr (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
+  return enc2<E5M2>(a, b) | (enc2<E5M2>(c, d) << 16);
+}
+
+// --------------------------------------------------- elements and vectors --
+
+enum DType { kBF16 = 0, kFP16 = 1, kFP32 = 2 };
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<kBF16> {
+  using T = __nv_bfloat16;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ float to_float(T v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ T from_float(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<kFP16> {
+  using T = __half;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ float to_float(T v) { return __half2float(v); }
+  static __device__ __forceinline__ T from_float(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<kFP32> {
+  using T = float;
+  static constexpr int kBytes = 4;
+  static __device__ __forceinline__ float to_float(T v) { return v; }
+  static __device__ __forceinline__ T from_float(float v) { return v; }
+};
+
+// N consecutive elements as they lie in memory (N * bytes a multiple of 16).
+template <int DT, int N>
+struct Vec {
+  using E = Elem<DT>;
+  static constexpr int kWords = N * E::kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // 16-byte aligned p, all N elements present; read once (no L1 allocation). Not the
+  // read-only path: an output may be the input in place.
+  __device__ __forceinline__ void load(const typename E::T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+          : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+          : "l"(reinterpret_cast<const char*>(p) + 4 * i));
+  }
+  // The first n elements, one at a time; the rest 0.
+  __device__ __forceinline__ void load_some(const typename E::T* p, int64_t n) {
+    zero();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) {
+        if constexpr (DT == kFP32) {
+          w[i] = __float_as_uint(p[i]);
+        } else {
+          const uint32_t b = reinterpret_cast<const uint16_t*>(p)[i];
+          w[i / 2] |= b << (16 * (i & 1));
+        }
+      }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (DT == kBF16) {
+      return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    } else if constexpr (DT == kFP16) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&w[i / 2]);
+      return (i & 1) ? __high2float(h) : __low2float(h);
+    } else {
+      return __uint_as_float(w[i]);
+    }
+  }
+  // Elements 2i and 2i + 1, each rounded to nearest even.
+  __device__ __forceinline__ void set2(int i, float lo, float hi) {
+    if constexpr (DT == kBF16) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    } else if constexpr (DT == kFP16) {
+      const __half2 v = __floats2half2_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      w[2 * i] = __float_as_uint(lo);
+      w[2 * i + 1] = __float_as_uint(hi);
+    }
+  }
+  __device__ __forceinline__ void store(typename E::T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+};
+
+}  // namespace t128
+}  // namespace mxk

@@ -293,6 +293,90 @@ int mx_quant_gemm_noalloc(const void* a_bf16, int scaling, const void* b_codes,
                           const uint8_t* b_scales, int64_t M, int64_t N, int64_t K, int out_fp32,
                           void* d, int* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * FP8 with one float scale per 128 elements: the operands of training and
+ * serving linear layers, next to the E8M0 formats above. Three operators that
+ * run one after the other: RMSNorm (or any producer) -> codes and scales ->
+ * GEMM; with what the backward pass of such a layer needs.
+ *
+ * Formats: MX_FMT_E4M3 (maxv 448) and MX_FMT_E5M2 (maxv 57344), one byte per
+ * element. A tile is 1 x 128: elements [128 j, 128 j + 128) of a row; a block
+ * is 128 x 128 of them. The last tile or block of a row or column may be
+ * short: rows and cols are free. Of a tile or block with largest magnitude
+ * amax:
+ *   scale  s = max(amax / maxv, 2^-126) rounded to float; with MX_POW2_SCALES
+ *          the smallest power of two >= 2^-126 with amax <= maxv s
+ *   code   RNE_sat(x / s), the quotient rounded to float first
+ *   a tile that holds NaN or Inf: s is NaN and every code NaN (0x7F)
+ * and code * s is the value. A zero tile has s = 2^-126 and codes +-0.
+ *
+ * Layouts. Codes: [rows, ld] bytes, ld a multiple of 16 and at least cols;
+ * the quantizers write each row's bytes up to cols rounded up to 16 (zeros
+ * past cols), nothing beyond. Tile scales are block-major: the scale of row r,
+ * tile j sits at scales[j * lds + r], lds a multiple of 4 and at least rows
+ * rounded up to 4 (the up to 3 floats past the last row may be written, and
+ * are read but not used). Block scales: row-major [ceil(rows/128),
+ * ceil(cols/128)], contiguous.
+ * Alignment: codes and tile scales 16 bytes, D 16 bytes, workspace 16 bytes,
+ * everything else its element. Rows that start on 16-byte boundaries are read
+ * fastest. MX_ERR_SHAPE: a pitch (ld...) too small or not such a multiple.
+ * Sizes below 2^31 per side and 2^40 elements. */
+typedef enum { MX_BF16 = 0, MX_FP16 = 1, MX_FP32 = 2 } mx_dtype_t;
+enum {
+  MX_BLOCK128 = 1 << 10,   /* a scale per 128 x 128 block (else per 1 x 128 tile) */
+  MX_POW2_SCALES = 1 << 11 /* power-of-two scales */
+};
+
+/* Quantize x [rows, cols] (row pitch ldx elements) along its rows into codes
+ * [rows, ldc] and scales, along its columns into codes_t [cols, ldct] and
+ * scales_t (the row-wise form of x transposed: tiles of 128 rows of a column),
+ * or both from one read. A NULL codes or codes_t leaves that form out. With
+ * MX_BLOCK128 both forms hold the same codes and scales, transposed. */
+int mx_quantize128(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int format,
+                   int flags, void* codes, int64_t ldc, float* scales, int64_t lds, void* codes_t,
+                   int64_t ldct, float* scales_t, int64_t ldst, void* stream);
+
+/* RMSNorm with the residual's addition and FP8 output. h = x + residual
+ * (NULL: x), y = h * weight / sqrt(mean(h^2) + eps); codes and scales are y's,
+ * in tiles. The norm uses the unrounded sum and the codes the unrounded y;
+ * h_out and y_out (each nullable) receive them rounded to x's type. x has row
+ * pitch ldx; residual, h_out and y_out are contiguous [rows, cols], all of
+ * type dtype, as is weight [cols]. h_out may be residual, or x when ldx ==
+ * cols (in place). flags: MX_POW2_SCALES or 0. */
+int mx_rms_norm_quant128(const void* x, int64_t ldx, const void* residual, const void* weight,
+                         int dtype, int64_t rows, int64_t cols, float eps, int format, int flags,
+                         void* h_out, void* y_out, void* codes, int64_t ldc, float* scales,
+                         int64_t lds, void* stream);
+
+/* Its gradient, straight through the quantizer: from grad_y = dL/dy and h,
+ *   n = h r, r = 1 / sqrt(mean(h^2) + eps),
+ *   grad_h = r (grad_y w - n mean(grad_y w n)) + grad_residual (NULL: 0),
+ *   grad_weight[c] = sum over rows of grad_y n, in float.
+ * grad_h is the gradient of x and of the residual alike; grad_residual is the
+ * gradient that reaches h_out from elsewhere. All [rows, cols] contiguous, of
+ * type dtype, weight [cols] too; grad_h may be grad_y or grad_residual (in
+ * place). workspace: mx_rms_norm_bwd_workspace(rows, cols) bytes (host only;
+ * -1 for a bad shape), free to reuse once the call's work is done. Results do
+ * not vary from run to run. */
+int64_t mx_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
+int mx_rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const void* grad_residual,
+                    int dtype, int64_t rows, int64_t cols, float eps, void* grad_h,
+                    float* grad_weight, void* workspace, void* stream);
+
+/* D[M, N] = A . B^T of two such operands on the tensor cores: A [M, K] with
+ * tile scales, B [N, K] with tile scales or (b_flags = MX_BLOCK128) block
+ * scales. Each K-block of 128 is multiplied with fp32 accumulation
+ * (tcgen05.mma.kind::f8f6f4) and added, times its two scales, to a float sum;
+ * D is row-major [M, N], bf16 (nearest even) or float (out_fp32 = 1). The
+ * forward and input-gradient products of a linear layer take block-scaled
+ * weights; its weight gradient two column-quantized operands. M, N, K are
+ * free; K == 0 writes zeros. status as in mx_gemm. Results do not vary from
+ * run to run on one GPU model. */
+int mx_gemm128(const void* a_codes, int64_t lda, const float* a_scales, int64_t ldsa, int a_format,
+               const void* b_codes, int64_t ldb, const float* b_scales, int64_t ldsb, int b_format,
+               int b_flags, int64_t M, int64_t N, int64_t K, int out_fp32, void* d, int* status,
+               void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* mx_status_string(int status);
 
