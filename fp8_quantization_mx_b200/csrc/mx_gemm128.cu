@@ -44,7 +44,8 @@ constexpr int kRows = 128;              // rows of a tile: the MMA's M
 constexpr uint32_t kBlockK = 128;       // elements (bytes) of K per stage
 constexpr uint32_t kTileP = kRows * kBlockK;
 
-constexpr int kStatusProducer = 11, kStatusMma = 12, kStatusSums = 13, kStatusDrain = 14;
+constexpr int kStatusProducer = 11, kStatusMma = 12, kStatusSums = 13, kStatusDrain = 14,
+              kStatusScales = 15;
 
 struct Gemm128Args {
   const float* p_scale;    // row side: tile scales [nk, p_ld] or block scales [., nk]
@@ -62,65 +63,86 @@ struct Gemm128Args {
   int vec;                 // rows of D start on 16-byte boundaries
 };
 
-template <int BN_, bool QCOL_, bool SWAP_, int S_>
+// BN columns per tile; QCOL: a scale per column; SWAP: the weights on the row
+// side; PAIR: two CTAs share a tile of 256 rows; S stages.
+template <int BN_, bool QCOL_, bool SWAP_, bool PAIR_, int S_>
 struct Cfg {
   static constexpr int BN = BN_, S = S_;
-  static constexpr bool QCOL = QCOL_, SWAP = SWAP_;   // QCOL: a scale per column
-  static constexpr int kHalves = BN >= 64 ? 2 : 1;
-  static constexpr int kWork = 4 * kHalves;           // accumulating warps
-  // 256 threads with up to 128 sums each need more than the 168 registers that
-  // 384 threads can have: the first warpgroup (TMA, MMA, two idle warps) gives
-  // most of its share to the other two. 128 (40 + 2 x 232) = 384 x 168.
+  static constexpr bool QCOL = QCOL_, SWAP = SWAP_, PAIR = PAIR_;
+  static constexpr int kCtas = PAIR ? 2 : 1;          // CTAs per tile (without a split)
+  static constexpr int kTileRows = kRows * kCtas;
+  // A pair's tile is multiplied in two halves of 128 columns, each with its own
+  // two accumulators, issuer and warps: an accumulator is used again after two
+  // K-blocks, and from its last MMA to its release takes longer than the other
+  // accumulator's MMAs cover when each is a whole K-block of 256 columns.
+  static constexpr int kHalves = PAIR ? 2 : 1;
+  static constexpr int kUnitN = BN / kHalves;         // columns per MMA
+  static constexpr int kBoxQ = kUnitN / kCtas;        // columns that a CTA loads at once
+    static constexpr int kParts = BN >= 64 ? 2 : 1;   // of the columns
+  static constexpr int kWork = 4 * kParts;            // accumulating warps
+  // 256 threads with 128 sums each need more than the 168 registers that 384
+  // threads can have: the first warpgroup (TMA, MMA, an idle warp) gives of its
+  // share. 128 x 56 + 256 x 224 = 384 x 168.
   static constexpr int kWork0 = 4;                    // first accumulating warp
-  static constexpr bool kShift = kHalves == 2;
+  static constexpr bool kShift = BN / kParts == 128;
   static constexpr int kThreads = (kWork0 + kWork) * 32;
-  static constexpr int kCols = BN / kHalves;          // columns per thread
-  static constexpr int NBUF = BN == 256 ? 2 : 4;      // accumulators in TMEM
+  static constexpr int kCols = BN / kParts;          // columns per thread
+  static constexpr int NBUF = PAIR ? 2 : 4;           // accumulators (of each half)
   static constexpr uint32_t kTmemCols = NBUF * BN;
-  static constexpr uint32_t kTileQ = BN * kBlockK;
+  static constexpr uint32_t kTileQ = kHalves * kBoxQ * kBlockK;
   static constexpr uint32_t kStage = kTileP + kTileQ;
-  static constexpr int QS = QCOL ? 8 : 0;             // column-scale slots
-  static constexpr uint32_t kQBytes = BN * 4;
-  static constexpr uint32_t kStgRow = QCOL ? 64 : 128;   // store staging: 32 such rows per warp
+  // Scales: a warp of its own puts four K-blocks at a time into one of two
+  // slots: per row (for blocks, times the scale of each 128 columns), and per
+  // column. The accumulating warps issue no loads: with the next scales' in
+  // flight a K-block took 130 ns longer.
+  static constexpr int kBatch = 4;
+  static constexpr int kRowSets = QCOL ? 1 : (BN + 127) / 128;
+  static constexpr uint32_t kSetBytes = kRows * 4;
+  static constexpr uint32_t kRowSlot = kBatch * kRowSets * kSetBytes;
+  static constexpr uint32_t kColSlot = QCOL ? kBatch * BN * 4 : 0;
+  static constexpr uint32_t kSlot = kRowSlot + kColSlot;
+  static constexpr uint32_t kStgRow = 64;             // store staging: 32 such rows per warp
   static constexpr uint32_t kStaging = SWAP ? 0 : kWork * 32 * kStgRow;
-  static constexpr int kBars = 2 * S + 2 * NBUF + 2 * QS + 1;
-  static constexpr uint32_t kSmem = S * kStage + kStaging + QS * kQBytes + 8 * kBars + 16 + 1024;
+  static constexpr int kBars = S + kHalves * (S + NBUF) + 1 + 4;
+  static constexpr uint32_t kSmem = S * kStage + kStaging + 2 * kSlot + 8 * kBars + 16 + 1024;
+  static_assert(kHalves == 1 || kParts == 2, "a half per part");
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(S * kStage >= kRows * BN * 4, "the split's partial tile reuses the ring");
+  static_assert(PAIR || S * kStage >= kRows * BN * 4, "the split's partial tile reuses the ring");
 };
 
 template <class C>
 struct Smem {
-  uint32_t raw, ring, stg, qv, bar;
+  uint32_t raw, ring, stg, scl, bar;
   uint32_t* tmem_holder;
   volatile int* abort_flag;
   uint8_t* ring_ptr;
   uint8_t* stg_ptr;
-  float* qv_ptr;
+  float* scl_ptr;
   __device__ explicit Smem(uint8_t* p) {
     raw = tc::smem_addr(p);
     ring = (raw + 1023u) & ~1023u;   // swizzle atoms need 1024-byte alignment
     stg = ring + C::S * C::kStage;
-    qv = stg + C::kStaging;
-    bar = qv + C::QS * C::kQBytes;
+    scl = stg + C::kStaging;
+    bar = scl + 2 * C::kSlot;
     ring_ptr = p + (ring - raw);
     stg_ptr = p + (stg - raw);
-    qv_ptr = reinterpret_cast<float*>(p + (qv - raw));
+    scl_ptr = reinterpret_cast<float*>(p + (scl - raw));
     tmem_holder = reinterpret_cast<uint32_t*>(p + (bar + 8u * C::kBars - raw));
     abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   }
   __device__ uint32_t p_tile(int s) const { return ring + s * C::kStage; }
   __device__ uint32_t q_tile(int s) const { return ring + s * C::kStage + kTileP; }
   __device__ uint32_t full(int s) const { return bar + 8u * s; }
-  __device__ uint32_t empty(int s) const { return bar + 8u * (C::S + s); }
-  __device__ uint32_t tfull(int b) const { return bar + 8u * (2 * C::S + b); }
-  __device__ uint32_t tempty(int b) const { return bar + 8u * (2 * C::S + C::NBUF + b); }
-  __device__ uint32_t done() const { return bar + 8u * (2 * C::S + 2 * C::NBUF); }
-  __device__ uint32_t qfull(int s) const { return bar + 8u * (2 * C::S + 2 * C::NBUF + 1 + s); }
-  __device__ uint32_t qempty(int s) const {
-    return bar + 8u * (2 * C::S + 2 * C::NBUF + 1 + C::QS + s);
+  // a stage's MMAs (of half h) are complete: its operands may go, its sums be read
+  __device__ uint32_t done(int h, int s) const { return bar + 8u * (C::S * (1 + h) + s); }
+  // accumulator b of half h may be overwritten
+  __device__ uint32_t tempty(int h, int b) const {
+    return bar + 8u * (C::S * (1 + C::kHalves) + C::NBUF * h + b);
   }
+  __device__ uint32_t last() const { return bar + 8u * (C::kBars - 5); }
+  __device__ uint32_t sfull(int s) const { return bar + 8u * (C::kBars - 4 + s); }
+  __device__ uint32_t sempty(int s) const { return bar + 8u * (C::kBars - 2 + s); }
 };
 
 // A position in a ring of N slots: the slot and the parity of its phase.
@@ -131,6 +153,12 @@ struct Ring {
   __device__ __forceinline__ void next() {
     if (++slot == N) {
       slot = 0;
+      par ^= 1;
+    }
+  }
+  __device__ __forceinline__ void prev() {
+    if (--slot < 0) {
+      slot = N - 1;
       par ^= 1;
     }
   }
@@ -150,30 +178,14 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t tiles_p, int64_t tile
   q = r / width;
 }
 
-// ------------------------------------------------- packed float arithmetic --
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// Two sums at once (packed multiply-add): a0 += f0 t0, a1 += f1 t1.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float f0, float f1, uint32_t t0,
+                                     uint32_t t1) {
+  const float2 v = __ffma2_rn(make_float2(f0, f1),
+                              make_float2(__uint_as_float(t0), __uint_as_float(t1)),
+                              make_float2(a0, a1));
+  a0 = v.x;
+  a1 = v.y;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -257,7 +269,7 @@ __device__ __forceinline__ void add_split(const Smem<C>& sm, const Gemm128Args& 
 // leaves as full 16-byte lanes of one run.
 template <class C, int ES>
 __device__ __forceinline__ void store_tile(const Smem<C>& sm, const Gemm128Args& g,
-                                           const uint64_t (&acc)[C::kCols / 2], int64_t p0,
+                                           const float (&acc)[C::kCols], int64_t p0,
                                            int64_t q0, int warp, int lane) {
   constexpr int kChunk = (C::kStgRow / ES < C::kCols) ? C::kStgRow / ES : C::kCols;
   constexpr int NJ = kChunk * ES / 16;          // 16-byte units per row
@@ -274,15 +286,9 @@ __device__ __forceinline__ void store_tile(const Smem<C>& sm, const Gemm128Args&
       uint32_t* w = &v.x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (ES == 2) {
-          float lo, hi;
-          unpack2(acc[(c0 + j * kPer) / 2 + i], lo, hi);
-          w[i] = bf16x2(lo, hi);
-        } else {
-          float lo, hi;
-          unpack2(acc[(c0 + j * kPer) / 2 + i / 2], lo, hi);
-          w[i] = __float_as_uint((i & 1) ? hi : lo);
-        }
+        const int at = c0 + j * kPer + i * (4 / ES);
+        if constexpr (ES == 2) w[i] = bf16x2(acc[at], acc[at + 1]);
+        else w[i] = __float_as_uint(acc[at]);
       }
       *reinterpret_cast<uint4*>(stg + lane * (NJ * 16) + ((j ^ (lane & (NJ - 1))) * 16)) = v;
     }
@@ -317,16 +323,14 @@ __device__ __forceinline__ void store_tile(const Smem<C>& sm, const Gemm128Args&
 // The same with D's rows on the column side: lane = consecutive columns of D.
 template <class C>
 __device__ __forceinline__ void store_tile_swapped(const Gemm128Args& g,
-                                                   const uint64_t (&acc)[C::kCols / 2], int64_t p0,
+                                                   const float (&acc)[C::kCols], int64_t p0,
                                                    int64_t q0, int warp, int lane) {
   const int64_t n = p0 + (warp & 3) * 32 + lane;
   const int64_t m0 = q0 + ((warp - C::kWork0) / 4) * C::kCols;
   if (n >= g.P) return;
 #pragma unroll
   for (int i = 0; i < C::kCols; ++i) {
-    float lo, hi;
-    unpack2(acc[i / 2], lo, hi);
-    const float v = (i & 1) ? hi : lo;
+    const float v = acc[i];
     if (m0 + i < g.Q) {
       const int64_t at = (m0 + i) * g.ldd + n;
       if (g.out_fp32)
@@ -343,220 +347,310 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                    const Gemm128Args g) {
   extern __shared__ uint8_t smem_raw[];
   const Smem<C> sm(smem_raw);
-  const int warp = threadIdx.x >> 5;
+  // (through a shuffle, so that the compiler keeps what follows from it in
+  // uniform registers, where tcgen05 and TMA operands have to be)
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
-  const int64_t tiles_p = (g.P + kRows - 1) / kRows;
+  const int64_t tiles_p = (g.P + C::kTileRows - 1) / C::kTileRows;
   const int64_t tiles_q = (g.Q + C::BN - 1) / C::BN;
   const int64_t ntiles = tiles_p * tiles_q;
-  // a cluster shares a tile: this CTA's K-blocks are [kb0, kb1)
-  const uint32_t rank = g.split > 1 ? blockIdx.x % g.split : 0;
-  const int64_t t_first = blockIdx.x / g.split;
-  const int64_t t_step = gridDim.x / g.split;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(g.nk) * rank / g.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(g.nk) * (rank + 1) / g.split);
+  // a cluster shares a tile: its CTAs take the rows in turn (PAIR) or split K,
+  // this one's K-blocks being [kb0, kb1)
+  const int shared = C::PAIR ? 2 : g.split;
+  const uint32_t rank = blockIdx.x % shared;
+  const int64_t t_first = blockIdx.x / shared;
+  const int64_t t_step = gridDim.x / shared;
+  const int kb0 = C::PAIR ? 0 : static_cast<int>(static_cast<int64_t>(g.nk) * rank / g.split);
+  const int kb1 = C::PAIR ? g.nk : static_cast<int>(static_cast<int64_t>(g.nk) * (rank + 1) / g.split);
+  const uint32_t row_rank = C::PAIR ? rank : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::S; ++s) {
-      tc::mbar_init(sm.full(s), 1);
-      tc::mbar_init(sm.empty(s), 1);
+    for (int s = 0; s < C::S; ++s) tc::mbar_init(sm.full(s), 1);
+    for (int h = 0; h < C::kHalves; ++h) {
+      for (int s = 0; s < C::S; ++s) tc::mbar_init(sm.done(h, s), 1);
+      for (int b = 0; b < C::NBUF; ++b)
+        tc::mbar_init(sm.tempty(h, b), C::kWork / C::kHalves * C::kCtas);
     }
-    for (int b = 0; b < C::NBUF; ++b) {
-      tc::mbar_init(sm.tfull(b), 1);
-      tc::mbar_init(sm.tempty(b), C::kWork);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(sm.sfull(s), 1);
+      tc::mbar_init(sm.sempty(s), C::kWork);
     }
-    for (int s = 0; s < C::QS; ++s) {
-      tc::mbar_init(sm.qfull(s), 1);
-      tc::mbar_init(sm.qempty(s), C::kWork);
-    }
-    tc::mbar_init(sm.done(), 1);
+    tc::mbar_init(sm.last(), 2);
     *sm.abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 1) tc::tmem_alloc(tc::smem_addr(sm.tmem_holder), C::kTmemCols);
+  if (warp == 1) {
+    if constexpr (C::PAIR) tc::tmem_alloc_pair(tc::smem_addr(sm.tmem_holder), C::kTmemCols);
+    else tc::tmem_alloc(tc::smem_addr(sm.tmem_holder), C::kTmemCols);
+  }
   tc::tc_fence_before();
   __syncthreads();
+  if constexpr (C::PAIR) tc::cluster_sync();   // the other CTA's barriers exist
   tc::tc_fence_after();
-  const uint32_t tmem = *sm.tmem_holder;
+  const uint32_t tmem = __shfl_sync(~0u, *sm.tmem_holder, 0);
 
   if (warp < C::kWork0) {
-    if constexpr (C::kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (C::kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      if (lane == 0) {
+      if (tc::elect_one()) {
         tc::prefetch_tmap(&tmP);
         tc::prefetch_tmap(&tmQ);
         Ring<C::S> st;
-        Ring<C::QCOL ? C::QS : 1> qs;
-        int64_t issued = 0, qissued = 0;
+        int issued = 0;   // this many of the last copies may be in flight
         bool ok = true;
         for (int64_t t = t_first; ok && t < ntiles; t += t_step) {
           int64_t p, q;
           tile_at(t, tiles_p, tiles_q, p, q);
-          const int p0 = static_cast<int>(p * kRows), q0 = static_cast<int>(q * C::BN);
-          // column scales present: the rest of the slot belongs to columns past the edge
-          const int64_t left = ((g.Q + 3) & ~int64_t(3)) - q0;
-          const uint32_t qbytes = static_cast<uint32_t>(left < C::BN ? left : C::BN) * 4;
+          const int p0 = static_cast<int>(p * C::kTileRows + row_rank * kRows);
+          const int q0 = static_cast<int>(q * C::BN);
           for (int kb = kb0; kb < kb1; ++kb) {
-            if (!tc::mbar_wait(sm.empty(st.slot), st.par ^ 1, sm.abort_flag, g.status, kStatusProducer)) {
-              ok = false;
-              break;
+            ok = tc::mbar_pass(sm.done(0, st.slot), st.par ^ 1, sm.abort_flag, g.status,
+                               kStatusProducer);
+            if constexpr (C::kHalves == 2)
+              ok = ok && tc::mbar_pass(sm.done(1, st.slot), st.par ^ 1, sm.abort_flag, g.status,
+                                       kStatusProducer);
+            if (!ok) break;
+            const int k0 = kb * static_cast<int>(kBlockK);
+            if constexpr (C::PAIR) {
+              // both CTAs' copies count on the first CTA's barrier, where the MMAs are issued
+              const uint32_t full = tc::mapa(sm.full(st.slot), 0);
+              if (rank == 0) tc::mbar_arrive_expect_tx(sm.full(st.slot), 2 * C::kStage);
+              tc::tma_load_2d_pair(sm.p_tile(st.slot), &tmP, k0, p0, full);
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                tc::tma_load_2d_pair(sm.q_tile(st.slot) + h * C::kBoxQ * kBlockK, &tmQ, k0,
+                                     q0 + h * C::kUnitN + static_cast<int>(rank) * C::kBoxQ, full);
+            } else {
+              tc::mbar_arrive_expect_tx(sm.full(st.slot), C::kStage);
+              tc::tma_load_2d(sm.p_tile(st.slot), &tmP, k0, p0, sm.full(st.slot));
+              tc::tma_load_2d(sm.q_tile(st.slot), &tmQ, k0, q0, sm.full(st.slot));
             }
-            tc::mbar_arrive_expect_tx(sm.full(st.slot), C::kStage);
-            tc::tma_load_2d(sm.p_tile(st.slot), &tmP, kb * static_cast<int>(kBlockK), p0, sm.full(st.slot));
-            tc::tma_load_2d(sm.q_tile(st.slot), &tmQ, kb * static_cast<int>(kBlockK), q0, sm.full(st.slot));
             st.next();
-            ++issued;
-            if constexpr (C::QCOL) {
-              if (!tc::mbar_wait(sm.qempty(qs.slot), qs.par ^ 1, sm.abort_flag, g.status,
-                                 kStatusProducer)) {
-                ok = false;
-                break;
-              }
-              tc::mbar_arrive_expect_tx(sm.qfull(qs.slot), qbytes);
-              tc::bulk_load(sm.qv + qs.slot * C::kQBytes, g.q_scale + kb * g.q_ld + q0, qbytes,
-                            sm.qfull(qs.slot));
-              qs.next();
-              ++qissued;
-            }
+            if (issued < C::S) ++issued;
           }
         }
-        // every copy this thread issued has landed before the CTA can exit
-        for (int64_t j = issued > C::S ? issued - C::S : 0; j < issued; ++j)
-          tc::mbar_wait(sm.full(static_cast<int>(j % C::S)), static_cast<uint32_t>(j / C::S) & 1,
-                        sm.abort_flag, g.status, kStatusDrain, false);
-        if constexpr (C::QCOL)
-          for (int64_t j = qissued > C::QS ? qissued - C::QS : 0; j < qissued; ++j)
-            tc::mbar_wait(sm.qfull(static_cast<int>(j % C::QS)), static_cast<uint32_t>(j / C::QS) & 1,
-                          sm.abort_flag, g.status, kStatusDrain, false);
+        // every copy issued has landed before the CTA can exit (PAIR: the first
+        // CTA sees to both CTAs' copies, and the other waits for it below)
+        for (int j = 0; j < (rank == 0 || !C::PAIR ? issued : 0); ++j) {
+          st.prev();
+          tc::mbar_wait(sm.full(st.slot), st.par, sm.abort_flag, g.status, kStatusDrain, false);
+        }
       }
       __syncwarp();
-    }
-    if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+    } else if (warp < 3 && row_rank == 0) {
+      // ------------------------------------------------------- MMA issuers
+      // Two threads, since one's waits, issue and commit take longer than the
+      // MMAs themselves: each has a half of the columns, or (one half) they
+      // take turns K-block by K-block.
+      if (tc::elect_one()) {
+        constexpr bool kTurns = C::kHalves == 1;
+        const int h = kTurns ? 0 : warp - 1;
         Ring<C::S> st;
         Ring<C::NBUF> tb;
-        bool ok = true;
-        for (int64_t t = t_first; ok && t < ntiles; t += t_step)
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!tc::mbar_wait(sm.tempty(tb.slot), tb.par ^ 1, sm.abort_flag, g.status, kStatusMma) ||
-                !tc::mbar_wait(sm.full(st.slot), st.par, sm.abort_flag, g.status, kStatusMma)) {
-              ok = false;
-              break;
-            }
-            tc::tc_fence_after();
-            const uint64_t pd = tc::kmajor_sw128_desc(sm.p_tile(st.slot));
-            const uint64_t qd = tc::kmajor_sw128_desc(sm.q_tile(st.slot));
+        int64_t todo = ((ntiles - t_first + t_step - 1) / t_step) * (kb1 - kb0);
+        if (kTurns && warp == 2) {
+          st.next();
+          tb.next();
+          --todo;
+        }
+        const uint64_t pd0 = tc::kmajor_sw128_desc(sm.p_tile(0));
+        const uint64_t qd0 = tc::kmajor_sw128_desc(sm.q_tile(0) + h * C::kBoxQ * kBlockK);
+        for (; todo > 0; todo -= kTurns ? 2 : 1) {
+          if (!tc::mbar_pass(sm.tempty(h, tb.slot), tb.par ^ 1, sm.abort_flag, g.status, kStatusMma) ||
+              !tc::mbar_pass(sm.full(st.slot), st.par, sm.abort_flag, g.status, kStatusMma))
+            break;
+          tc::tc_fence_after();
+          const uint64_t pd = pd0 + st.slot * (C::kStage >> 4);
+          const uint64_t qd = qd0 + st.slot * (C::kStage >> 4);
+          const uint32_t d = tmem + (h * C::NBUF + tb.slot) * C::kUnitN;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)   // K = 32: 32 bytes further along the rows
-              tc::mma_f8(tmem + tb.slot * C::BN, pd + 2 * k, qd + 2 * k, g.idesc, k != 0);
-            tc::tc_commit(sm.empty(st.slot));
-            tc::tc_commit(sm.tfull(tb.slot));
+          for (int k = 0; k < 4; ++k) {   // K = 32: 32 bytes further along the rows
+            if constexpr (C::PAIR) tc::mma_f8_pair(d, pd + 2 * k, qd + 2 * k, g.idesc, k != 0);
+            else tc::mma_f8(d, pd + 2 * k, qd + 2 * k, g.idesc, k != 0);
+          }
+          if constexpr (C::PAIR) tc::tc_commit_pair(sm.done(h, st.slot), 3);
+          else tc::tc_commit(sm.done(h, st.slot));
+          st.next();
+          tb.next();
+          if constexpr (kTurns) {
             st.next();
             tb.next();
           }
+        }
         // every MMA has finished before TMEM is freed, whatever ended the loop
-        tc::tc_commit(sm.done());
-        tc::mbar_wait(sm.done(), 0, sm.abort_flag, g.status, kStatusDrain, false);
+        if constexpr (C::PAIR) tc::tc_commit_pair(sm.last(), 1);
+        else tc::tc_commit(sm.last());
+        tc::mbar_wait(sm.last(), 0, sm.abort_flag, g.status, kStatusDrain, false);
       }
+      __syncwarp();
+    }
+    if (warp == 3) {
+      // ------------------------------------------------------------ scales
+      Ring<2> ss;
+      int issued = 0;
+      bool ok = true;
+      for (int64_t t = t_first; ok && t < ntiles; t += t_step) {
+        int64_t p, q;
+        tile_at(t, tiles_p, tiles_q, p, q);
+        const int64_t p0 = p * C::kTileRows + row_rank * kRows, q0 = q * C::BN;
+        for (int kb = kb0; kb < kb1; kb += C::kBatch) {
+          // four rows' scales per lane and K-block; block scales one per lane
+          float a[C::kBatch][4], b = 1.0f;
+#pragma unroll
+          for (int i = 0; i < C::kBatch; ++i) {
+            const int k = kb + i < kb1 ? kb + i : kb1 - 1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int64_t row = p0 + j * 32 + lane;
+              a[i][j] = g.p_block ? g.p_scale[p * g.nk + k]
+                                  : g.p_scale[k * g.p_ld + (row < g.P ? row : g.P - 1)];
+            }
+          }
+          if constexpr (!C::QCOL) {
+            const int64_t col = q0 + (lane / C::kBatch) * kRows;
+            const int k = kb + lane % C::kBatch < kb1 ? kb + lane % C::kBatch : kb1 - 1;
+            if (lane < C::kBatch * C::kRowSets)
+              b = g.q_scale[(col < g.Q ? col : g.Q - 1) / kRows * g.nk + k];
+          }
+          if (!__all_sync(~0u, tc::mbar_pass(sm.sempty(ss.slot), ss.par ^ 1, sm.abort_flag, g.status,
+                                             kStatusScales))) {
+            ok = false;
+            break;
+          }
+          float* slot = sm.scl_ptr + ss.slot * (C::kSlot / 4);
+#pragma unroll
+          for (int i = 0; i < C::kBatch; ++i)
+#pragma unroll
+            for (int n = 0; n < C::kRowSets; ++n) {
+              const float f = C::QCOL ? 1.0f : __shfl_sync(~0u, b, n * C::kBatch + i);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                slot[(i * C::kRowSets + n) * kRows + j * 32 + lane] = C::QCOL ? a[i][j] : a[i][j] * f;
+            }
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (C::QCOL) {
+              // the columns' present: the rest of a slot belongs to columns past the edge
+              const int64_t left = ((g.Q + 3) & ~int64_t(3)) - q0;
+              const uint32_t bytes = static_cast<uint32_t>(left < C::BN ? left : C::BN) * 4;
+              const int n = kb1 - kb < C::kBatch ? kb1 - kb : C::kBatch;
+              tc::mbar_arrive_expect_tx(sm.sfull(ss.slot), n * bytes);
+              for (int i = 0; i < n; ++i)
+                tc::bulk_load(sm.scl + ss.slot * C::kSlot + C::kRowSlot + i * C::BN * 4,
+                              g.q_scale + (kb + i) * g.q_ld + q0, bytes, sm.sfull(ss.slot));
+            } else {
+              tc::mbar_arrive(sm.sfull(ss.slot));
+            }
+          }
+          ss.next();
+          if (issued < 2) ++issued;
+        }
+      }
+      if (C::QCOL && lane == 0)   // copies landed before the CTA can exit
+        for (int j = 0; j < issued; ++j) {
+          ss.prev();
+          tc::mbar_wait(sm.sfull(ss.slot), ss.par, sm.abort_flag, g.status, kStatusDrain, false);
+        }
       __syncwarp();
     }
     // (accumulators read, by the other branch's half of this barrier)
     tc::named_sync(1, C::kThreads);
+    if constexpr (C::PAIR) tc::cluster_sync();   // and by the other CTA, whose copies have landed
     if (warp == 1) {
       tc::tc_fence_after();
-      tc::tmem_dealloc(tmem, C::kTmemCols);
+      if constexpr (C::PAIR) tc::tmem_dealloc_pair(tmem, C::kTmemCols);
+      else tc::tmem_dealloc(tmem, C::kTmemCols);
     }
-    if (g.split > 1) {
+    if (!C::PAIR && g.split > 1) {
       tc::cluster_sync();
       tc::cluster_sync();
     }
   } else {
     // ------------------------------------------------------ scaled sums
-    if constexpr (C::kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    const int quarter = warp & 3, half = (warp - C::kWork0) / 4;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * C::kCols;
+    if constexpr (C::kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3, part = (warp - C::kWork0) / 4;
+    const int h = C::kHalves == 2 ? part : 0;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               (C::kHalves == 2 ? h * C::NBUF * C::kUnitN : part * C::kCols);
+    Ring<C::S> st;
     Ring<C::NBUF> tb;
-    Ring<C::QCOL ? C::QS : 1> qs;
+    Ring<2> ss;
+    // where accumulators are given back: to the CTA that issues the MMAs
+    const uint32_t free0 = C::PAIR ? tc::mapa(sm.tempty(h, 0), 0) : sm.tempty(h, 0);
+    // this thread's row scale and its part's column scales in a slot
+    const float* row_scale =
+        sm.scl_ptr + (C::QCOL ? 0 : part * C::kCols / kRows) * kRows + quarter * 32 + lane;
+    const float* col_scale = sm.scl_ptr + C::kRowSlot / 4 + part * C::kCols;
     bool ok = true;
     for (int64_t t = t_first; ok && t < ntiles; t += t_step) {
       int64_t p, q;
       tile_at(t, tiles_p, tiles_q, p, q);
-      const int64_t p0 = p * kRows, q0 = q * C::BN;
-      // this row's scale, and (blocks on the column side) the columns'
-      const int64_t row = p0 + quarter * 32 + lane;
-      const int64_t prow = row < g.P ? row : g.P - 1;
-      const float* ps = g.p_block ? g.p_scale + p * g.nk : g.p_scale + prow;
-      const int64_t pstep = g.p_block ? 1 : g.p_ld;
-      const int64_t qcol = q0 + half * C::kCols;
-      const float* qb = C::QCOL ? nullptr
-                                : g.q_scale + (qcol < g.Q ? qcol : g.Q - 1) / kRows * g.nk;
-      uint64_t acc[C::kCols / 2];
+      const int64_t p0 = p * C::kTileRows + row_rank * kRows, q0 = q * C::BN;
+      float acc[C::kCols];
 #pragma unroll
-      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
-      float s_next = kb0 < kb1 ? ps[kb0 * pstep] : 0.0f;
-      float b_next = !C::QCOL && kb0 < kb1 ? qb[kb0] : 1.0f;
+      for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const float s = C::QCOL ? s_next : s_next * b_next;
-        if (kb + 1 < kb1) {
-          s_next = ps[(kb + 1) * pstep];
-          if (!C::QCOL) b_next = qb[kb + 1];
-        }
-        bool got = true;
-        if constexpr (C::QCOL)
-          got = tc::mbar_wait(sm.qfull(qs.slot), qs.par, sm.abort_flag, g.status, kStatusSums);
-        got = got && tc::mbar_wait(sm.tfull(tb.slot), tb.par, sm.abort_flag, g.status, kStatusSums);
-        // one decision for the warp: tcgen05.ld is a whole-warp instruction
-        if (!__all_sync(~0u, got)) {
-          ok = false;
-          break;
-        }
+        const int at = (kb - kb0) & (C::kBatch - 1);
+        const bool last = at == C::kBatch - 1 || kb + 1 == kb1;   // of its slot
+        if (at == 0)
+          ok &= tc::mbar_wait(sm.sfull(ss.slot), ss.par, sm.abort_flag, g.status, kStatusSums);
+        const int slot = ss.slot * (C::kSlot / 4);
+        const float s = row_scale[slot + at * C::kRowSets * kRows];
+        // (after a wait that ran out the loop goes on, every later wait returns
+        // at once, and nothing is stored: tcgen05.ld needs the whole warp)
+        ok &= tc::mbar_wait(sm.done(h, st.slot), st.par, sm.abort_flag, g.status, kStatusSums);
+        __syncwarp();
         tc::tc_fence_after();
-        const uint64_t s2 = pack2(s, s);
-        constexpr int kLd = C::kCols < 32 ? C::kCols : 32;
+        constexpr int kLd = C::kCols < 32 ? 16 : 32;   // columns per load, two in flight
+        const uint32_t taddr = lane_base + tb.slot * C::kUnitN;
+        uint32_t r[2][kLd];
+        tc::tmem_ld_start(taddr, r[0]);
+        tc::tmem_ld_wait(r[0]);
 #pragma unroll
         for (int c0 = 0; c0 < C::kCols; c0 += kLd) {
-          uint32_t r[kLd];
-          const uint32_t taddr = lane_base + tb.slot * C::BN + c0;
-          if constexpr (kLd == 32) tc::tmem_ld32(taddr, r);
-          else tc::tmem_ld16(taddr, r);
-          if constexpr (C::QCOL) {
-            const float4* qv = reinterpret_cast<const float4*>(sm.qv_ptr + qs.slot * C::BN +
-                                                               half * C::kCols + c0);
-#pragma unroll
-            for (int i = 0; i < kLd / 4; ++i) {
-              const float4 f = qv[i];
-              acc[(c0 + 4 * i) / 2] = fma2(mul2(pack2(f.x, f.y), s2), pack2u(r[4 * i], r[4 * i + 1]),
-                                           acc[(c0 + 4 * i) / 2]);
-              acc[(c0 + 4 * i) / 2 + 1] =
-                  fma2(mul2(pack2(f.z, f.w), s2), pack2u(r[4 * i + 2], r[4 * i + 3]),
-                       acc[(c0 + 4 * i) / 2 + 1]);
-            }
+          uint32_t(&now)[kLd] = r[(c0 / kLd) & 1];
+          uint32_t(&next)[kLd] = r[(c0 / kLd + 1) & 1];
+          if (c0 + kLd < C::kCols) {
+            tc::tmem_ld_start(taddr + c0 + kLd, next);
           } else {
-#pragma unroll
-            for (int i = 0; i < kLd / 2; ++i)
-              acc[c0 / 2 + i] = fma2(s2, pack2u(r[2 * i], r[2 * i + 1]), acc[c0 / 2 + i]);
+            // the accumulator has been read
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (C::PAIR) tc::mbar_arrive_relaxed_cluster(free0 + 8 * tb.slot);
+              else tc::mbar_arrive_relaxed(free0 + 8 * tb.slot);
+            }
           }
+          const float4* qv = reinterpret_cast<const float4*>(col_scale + slot + at * C::BN + c0);
+#pragma unroll
+          for (int i = 0; i < kLd; i += 4) {
+            float4 f = make_float4(s, s, s, s);
+            if constexpr (C::QCOL) {
+              f = qv[i / 4];
+              f.x *= s, f.y *= s, f.z *= s, f.w *= s;
+            }
+            fma2(acc[c0 + i], acc[c0 + i + 1], f.x, f.y, now[i], now[i + 1]);
+            fma2(acc[c0 + i + 2], acc[c0 + i + 3], f.z, f.w, now[i + 2], now[i + 3]);
+          }
+          if (c0 + kLd < C::kCols) tc::tmem_ld_wait(next);
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(sm.tempty(tb.slot));
-          if constexpr (C::QCOL) tc::mbar_arrive(sm.qempty(qs.slot));
+        if (last) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(sm.sempty(ss.slot));
+          ss.next();
         }
+        st.next();
         tb.next();
-        if constexpr (C::QCOL) qs.next();
       }
-      if (!ok) break;
-      if (g.split > 1) {
+      if (!__all_sync(~0u, ok)) break;
+      if (!C::PAIR && g.split > 1) {
         // the ring is idle: every K-block loaded has been multiplied. (The
         // generic writes below follow the MMAs' reads through tfull.)
 #pragma unroll
         for (int i = 0; i < C::kCols; i += 4) {
-          float4 v;
-          unpack2(acc[i / 2], v.x, v.y);
-          unpack2(acc[i / 2 + 1], v.z, v.w);
-          const int c = half * C::kCols + i, r = quarter * 32 + lane;
+          const float4 v = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          const int c = part * C::kCols + i, r = quarter * 32 + lane;
           if constexpr (C::SWAP) {
             const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -575,7 +669,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     tc::tc_fence_before();
     tc::named_sync(1, C::kThreads);
-    if (g.split > 1) {
+    if constexpr (C::PAIR) {
+      tc::cluster_sync();
+    } else if (g.split > 1) {
       int64_t p, q;
       tile_at(t_first, tiles_p, tiles_q, p, q);
       tc::cluster_sync();   // every partial tile is in shared memory
@@ -653,10 +749,10 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
   const bool maps = C::SWAP ? codes_map(&tmP, u.b, u.N, u.K, u.ldb, kRows) &&
                                   codes_map(&tmQ, u.a, u.M, u.K, u.lda, C::BN)
                             : codes_map(&tmP, u.a, u.M, u.K, u.lda, kRows) &&
-                                  codes_map(&tmQ, u.b, u.N, u.K, u.ldb, C::BN);
+                                  codes_map(&tmQ, u.b, u.N, u.K, u.ldb, C::kBoxQ);
   if (!maps) return cudaErrorInvalidValue;
   const uint32_t fa = u.a_e5m2 ? 1 : 0, fb = u.b_e5m2 ? 1 : 0;
-  g.idesc = tc::idesc_f8(kRows, C::BN, C::SWAP ? fb : fa, C::SWAP ? fa : fb);
+  g.idesc = tc::idesc_f8(C::kTileRows, C::kUnitN, C::SWAP ? fb : fa, C::SWAP ? fa : fb);
   g.P = C::SWAP ? u.N : u.M;
   g.Q = C::SWAP ? u.M : u.N;
   g.p_scale = C::SWAP ? u.b_scales : u.a_scales;
@@ -664,21 +760,23 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
   g.p_ld = C::SWAP ? u.ldsb : u.ldsa;
   g.q_ld = C::SWAP ? u.ldsa : u.ldsb;
   g.p_block = C::SWAP ? u.b_block : 0;
-  const int64_t tiles = ((g.P + kRows - 1) / kRows) * ((g.Q + C::BN - 1) / C::BN);
+  const int64_t tiles = ((g.P + C::kTileRows - 1) / C::kTileRows) * ((g.Q + C::BN - 1) / C::BN);
+  const int cluster = C::PAIR ? 2 : g.split;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(g.split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = g.split > 1 ? 1 : 0;
-  // one tile per cluster, or (no split) persistent CTAs, one per SM
-  if (g.split > 1 && tiles * g.split > 0x7fffffff) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3(static_cast<unsigned>(g.split > 1 ? tiles * g.split : tiles < sms ? tiles : sms));
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  // one tile per cluster that splits K; else persistent CTAs, one per SM
+  if (tiles > 0x7fffffff / 8) return cudaErrorInvalidValue;
+  const int64_t most = g.split > 1 ? tiles : sms / cluster;
+  cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * cluster));
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmP, tmQ, g);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -715,18 +813,18 @@ cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t s
   g.out_fp32 = u.out_fp32;
   g.vec = u.N * (u.out_fp32 ? 4 : 2) % 16 == 0;
   if (p.swap) {
-    if (p.bn == 16) return launch<Cfg<16, true, true, 10>>(u, g, dev, sms, st);
-    if (p.bn == 32) return launch<Cfg<32, true, true, 10>>(u, g, dev, sms, st);
-    return launch<Cfg<64, true, true, 8>>(u, g, dev, sms, st);
+    if (p.bn == 16) return launch<Cfg<16, true, true, false, 10>>(u, g, dev, sms, st);
+    if (p.bn == 32) return launch<Cfg<32, true, true, false, 10>>(u, g, dev, sms, st);
+    return launch<Cfg<64, true, true, false, 8>>(u, g, dev, sms, st);
   }
   if (u.b_block) {
-    if (p.bn == 64) return launch<Cfg<64, false, false, 8>>(u, g, dev, sms, st);
-    if (p.bn == 128) return launch<Cfg<128, false, false, 6>>(u, g, dev, sms, st);
-    return launch<Cfg<256, false, false, 4>>(u, g, dev, sms, st);
+    if (p.bn == 64) return launch<Cfg<64, false, false, false, 8>>(u, g, dev, sms, st);
+    if (p.bn == 128) return launch<Cfg<128, false, false, false, 6>>(u, g, dev, sms, st);
+    return launch<Cfg<256, false, false, true, 6>>(u, g, dev, sms, st);
   }
-  if (p.bn == 64) return launch<Cfg<64, true, false, 8>>(u, g, dev, sms, st);
-  if (p.bn == 128) return launch<Cfg<128, true, false, 6>>(u, g, dev, sms, st);
-  return launch<Cfg<256, true, false, 4>>(u, g, dev, sms, st);
+  if (p.bn == 64) return launch<Cfg<64, true, false, false, 8>>(u, g, dev, sms, st);
+  if (p.bn == 128) return launch<Cfg<128, true, false, false, 6>>(u, g, dev, sms, st);
+  return launch<Cfg<256, true, false, true, 6>>(u, g, dev, sms, st);
 }
 
 }  // namespace mxk
