@@ -34,6 +34,7 @@
 
 #include "mx_gemm128.h"
 #include "mx_launch.h"
+#include "mx_pdl.cuh"
 #include "mx_tc.cuh"
 
 namespace mxk {
@@ -388,6 +389,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if constexpr (C::PAIR) tc::cluster_sync();   // the other CTA's barriers exist
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *sm.tmem_holder, 0);
+  dependent_launch();
+  dependent_wait();   // operands, scales and D from here on
 
   if (warp < C::kWork0) {
     if constexpr (C::kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -762,23 +765,11 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
   g.p_block = C::SWAP ? u.b_block : 0;
   const int64_t tiles = ((g.P + C::kTileRows - 1) / C::kTileRows) * ((g.Q + C::BN - 1) / C::BN);
   const int cluster = C::PAIR ? 2 : g.split;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
   // one tile per cluster that splits K; else persistent CTAs, one per SM
   if (tiles > 0x7fffffff / 8) return cudaErrorInvalidValue;
   const int64_t most = g.split > 1 ? tiles : sms / cluster;
-  cfg.gridDim = dim3(static_cast<unsigned>((tiles < most ? tiles : most) * cluster));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmP, tmQ, g);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>((tiles < most ? tiles : most) * cluster);
+  return launch_dependent(kern, dim3(grid), dim3(C::kThreads), C::kSmem, st, cluster, tmP, tmQ, g);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "mx_launch.h"
+#include "mx_pdl.cuh"
 #include "mx_tile128.cuh"
 
 namespace mxk {
@@ -66,12 +67,18 @@ __device__ __forceinline__ float row_rstd(float sum, int64_t cols, float eps) {
   return __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(cols)) + eps);
 }
 
-template <bool E5M2, bool SLOW>
-__device__ __forceinline__ uint2 encode8(const float (&y)[8], float s, float inv) {
-  float q[8];
+template <bool E5M2>
+__device__ __forceinline__ uint2 encode8(const float (&y)[8], const Divisor& d) {
+  const float2 s = make_float2(d.s, d.s), inv = make_float2(d.inv, d.inv);
+  float2 q[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = div_scale<SLOW>(y[i], s, inv);
-  return make_uint2(enc4<E5M2>(q[0], q[1], q[2], q[3]), enc4<E5M2>(q[4], q[5], q[6], q[7]));
+  for (int i = 0; i < 4; ++i) {
+    float2 x = make_float2(y[2 * i], y[2 * i + 1]);
+    if (d.slow) x = __fmul2_rn(x, make_float2(kLift, kLift));
+    q[i] = div2(x, s, inv);
+  }
+  return make_uint2(enc4<E5M2>(q[0].x, q[0].y, q[1].x, q[1].y),
+                    enc4<E5M2>(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
 // One CTA per row, NV vectors of 8 elements per thread: the vectors of a tile
@@ -81,6 +88,8 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm128_kernel(const Norm
   using T = typename Elem<DT>::T;
   __shared__ float red[32];
   const int tid = threadIdx.x, nt = blockDim.x;
+  dependent_launch();
+  dependent_wait();
   const int64_t row = blockIdx.x;
   const int nvec = static_cast<int>(a.cols / 8);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -133,8 +142,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm128_kernel(const Norm
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
     const float s = tile_scale<E5M2>(m, a.pow2);
-    const float inv = recip(s);
-    const uint2 c = s < kSlowScale ? encode8<E5M2, true>(y, s, inv) : encode8<E5M2, false>(y, s, inv);
+    const uint2 c = encode8<E5M2>(y, divisor(s, m == 0.0f));
     // codes up to the row's padding to 16 bytes (the vector past the last is 0)
     if (8 * static_cast<int64_t>(i) < ((a.cols + 15) & ~int64_t(15)))
       *reinterpret_cast<uint2*>(a.codes + row * a.ldc + 8 * i) = c;
@@ -158,6 +166,8 @@ __global__ void __launch_bounds__(256) norm128_any_kernel(const NormArgs a) {
   using T = typename E::T;
   __shared__ float red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dependent_launch();
+  dependent_wait();
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
@@ -222,6 +232,8 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_bwd_kernel(const Nor
   using T = typename Elem<DT>::T;
   __shared__ float red[2][64];
   const int tid = threadIdx.x, nt = blockDim.x;
+  dependent_launch();
+  dependent_wait();
   const int nvec = static_cast<int>(a.cols / 8);
   const T* gy = static_cast<const T*>(a.gy);
   const T* hh = static_cast<const T*>(a.h);
@@ -339,6 +351,8 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(const NormBwdArgs a) 
   using E = Elem<DT>;
   using T = typename E::T;
   __shared__ float red[2][64];
+  dependent_launch();
+  dependent_wait();
   const T* w = static_cast<const T*>(a.weight);
   float* part = a.part + blockIdx.x * a.cols;
   int par = 0;
@@ -370,6 +384,8 @@ __global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, in
                                                            int64_t cols, float* gw) {
   __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dependent_launch();
+  dependent_wait();
   const int64_t c = blockIdx.x * int64_t(32) + lane;
   float s = 0.0f;
   if (c < cols) {
@@ -398,18 +414,14 @@ unsigned threads(int64_t nvec, int nv) {
 
 template <int DT, bool E5M2>
 cudaError_t launch_norm(const NormArgs& a, bool vec, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(a.rows);
-  if (!vec) {
-    norm128_any_kernel<DT, E5M2><<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError();
-  }
+  const dim3 grid(static_cast<unsigned>(a.rows));
+  if (!vec) return launch_dependent(norm128_any_kernel<DT, E5M2>, grid, dim3(256), 0, st, 1, a);
   const int64_t nvec = (a.cols + 15) / 16 * 2;   // with the codes' padding
   const int nv = vectors(nvec);
-  const unsigned nt = threads(nvec, nv);
-  if (nv == 1) norm128_kernel<DT, E5M2, 1><<<grid, nt, 0, st>>>(a);
-  else if (nv == 2) norm128_kernel<DT, E5M2, 2><<<grid, nt, 0, st>>>(a);
-  else norm128_kernel<DT, E5M2, 4><<<grid, nt, 0, st>>>(a);
-  return cudaGetLastError();
+  const auto kern = nv == 1   ? norm128_kernel<DT, E5M2, 1>
+                    : nv == 2 ? norm128_kernel<DT, E5M2, 2>
+                              : norm128_kernel<DT, E5M2, 4>;
+  return launch_dependent(kern, grid, dim3(threads(nvec, nv)), 0, st, 1, a);
 }
 
 // CTAs: as many as the SMs hold at once (registers: 768 threads with one
@@ -425,27 +437,26 @@ cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaS
   }
   if (most > kNormParts) most = kNormParts;
   const int grid = static_cast<int>(a.rows < most ? a.rows : most);
+  cudaError_t e;
   if (!vec) {
-    norm_bwd_any_kernel<DT><<<grid, 256, 0, st>>>(a);
+    e = launch_dependent(norm_bwd_any_kernel<DT>, dim3(grid), dim3(256), 0, st, 1, a);
   } else {
     const int64_t nvec = a.cols / 8;
     const int nv = vectors(nvec);
     const unsigned nt = threads(nvec, nv);
-    if (nv == 1) norm_bwd_kernel<DT, 1><<<grid, nt, 0, st>>>(a);
-    else if (nv == 2) norm_bwd_kernel<DT, 2><<<grid, nt, 0, st>>>(a);
-    else {
-      const int smem = static_cast<int>(nt) * 4 * 8 * 4;   // up to 64 KiB
-      const cudaError_t e = cudaFuncSetAttribute(
-          norm_bwd_kernel<DT, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 8 * 4);
+    const auto kern = nv == 1   ? norm_bwd_kernel<DT, 1>
+                      : nv == 2 ? norm_bwd_kernel<DT, 2>
+                                : norm_bwd_kernel<DT, 4>;
+    const size_t smem = nv == 4 ? nt * size_t(4 * 8 * 4) : 0;   // up to 64 KiB
+    if (smem) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 8 * 4);
       if (e != cudaSuccess) return e;
-      norm_bwd_kernel<DT, 4><<<grid, nt, smem, st>>>(a);
     }
+    e = launch_dependent(kern, dim3(grid), dim3(nt), smem, st, 1, a);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_bwd_sum_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 256, 0, st>>>(a.part, grid,
-                                                                                 a.cols, gw);
-  return cudaGetLastError();
+  return launch_dependent(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)),
+                          dim3(256), 0, st, 1, a.part, grid, a.cols, gw);
 }
 
 }  // namespace

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "mx_launch.h"
+#include "mx_pdl.cuh"
 #include "mx_tile128.cuh"
 
 namespace mxk {
@@ -53,43 +54,53 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ int word_at(int c, int g) { return c * 32 + (g ^ (((c >> 4) & 7) << 2)); }
 
 template <bool E5M2, bool SLOW, int DT>
-__device__ __forceinline__ uint4 encode_row(const Vec<DT, 16>& v, float s, float inv) {
+__device__ __forceinline__ uint4 encode_row(const Vec<DT, 16>& v, const Divisor& d) {
   uint32_t o[4];
+  const float2 s = make_float2(d.s, d.s), inv = make_float2(d.inv, d.inv);
+  const float2 lift = make_float2(kLift, kLift);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = enc4<E5M2>(div_scale<SLOW>(v.get(4 * i), s, inv), div_scale<SLOW>(v.get(4 * i + 1), s, inv),
-                      div_scale<SLOW>(v.get(4 * i + 2), s, inv),
-                      div_scale<SLOW>(v.get(4 * i + 3), s, inv));
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = div2(SLOW ? __fmul2_rn(v.get2(2 * i), lift) : v.get2(2 * i), s, inv);
+    const float2 b = div2(SLOW ? __fmul2_rn(v.get2(2 * i + 1), lift) : v.get2(2 * i + 1), s, inv);
+    o[i] = enc4<E5M2>(a.x, a.y, b.x, b.y);
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// col_s, col_inv: of the piece's columns, lifted where the scale is tiny (SLOW
+// takes notice).
 template <bool E5M2, bool SLOW, int DT>
 __device__ __forceinline__ void encode_cols(const Vec<DT, 16> (&v)[4], const float* col_s,
-                                            const float* col_inv, int g, int sub, uint32_t* out) {
+                                            const float* col_inv, const float* col_lift, int g,
+                                            int sub, uint32_t* out) {
 #pragma unroll
-  for (int c4 = 0; c4 < 4; ++c4) {
-    const float4 s = reinterpret_cast<const float4*>(col_s)[sub * 4 + c4];
-    const float4 inv = reinterpret_cast<const float4*>(col_inv)[sub * 4 + c4];
-    const float ss[4] = {s.x, s.y, s.z, s.w}, ii[4] = {inv.x, inv.y, inv.z, inv.w};
+  for (int c2 = 0; c2 < 8; ++c2) {
+    const float2 s = reinterpret_cast<const float2*>(col_s)[sub * 8 + c2];
+    const float2 inv = reinterpret_cast<const float2*>(col_inv)[sub * 8 + c2];
+    float2 q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = 4 * c4 + j;
-      out[word_at(sub * 16 + c, g)] = enc4<E5M2>(
-          div_scale<SLOW>(v[0].get(c), ss[j], ii[j]), div_scale<SLOW>(v[1].get(c), ss[j], ii[j]),
-          div_scale<SLOW>(v[2].get(c), ss[j], ii[j]), div_scale<SLOW>(v[3].get(c), ss[j], ii[j]));
+    for (int i = 0; i < 4; ++i) {
+      float2 x = v[i].get2(c2);
+      if constexpr (SLOW) x = __fmul2_rn(x, reinterpret_cast<const float2*>(col_lift)[sub * 8 + c2]);
+      q[i] = div2(x, s, inv);
     }
+    out[word_at(sub * 16 + 2 * c2, g)] = enc4<E5M2>(q[0].x, q[1].x, q[2].x, q[3].x);
+    out[word_at(sub * 16 + 2 * c2 + 1, g)] = enc4<E5M2>(q[0].y, q[1].y, q[2].y, q[3].y);
   }
 }
 
 template <int DT, bool E5M2, bool ROWS, bool COLS, bool BLOCK>
-__global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a) {
+__global__ void __launch_bounds__(kThreads, 3) quant128_kernel(const Quant128Args a) {
   using T = typename Elem<DT>::T;
   __shared__ __align__(16) uint32_t sh_codes[COLS ? 128 * 32 : 4];
   __shared__ __align__(16) float sh_red[8][BLOCK ? 4 : 128];
-  __shared__ __align__(16) float sh_s[128], sh_inv[128];
+  __shared__ __align__(16) float sh_s[COLS ? 128 : 4], sh_inv[COLS ? 128 : 4], sh_lift[COLS ? 128 : 4];
+  __shared__ int sh_slow;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = tid >> 3, sub = tid & 7;
+  dependent_launch();
+  dependent_wait();
   const int64_t rb = blockIdx.x / a.nbc, cb = blockIdx.x % a.nbc;
   const int64_t row0 = rb * 128 + 4 * g, col0 = cb * 128 + 16 * sub;
 
@@ -109,9 +120,7 @@ __global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a
   if constexpr (BLOCK) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < 16; ++c) m = amax2(m, v[i].get(c));
+    for (int i = 0; i < 4; ++i) m = amax2(m, v[i].amax());
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
     if (lane == 0) sh_red[warp][0] = m;
@@ -119,14 +128,10 @@ __global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = amax2(m, sh_red[w][0]);
     const float s = tile_scale<E5M2>(m, a.pow2);
-    const float inv = recip(s);
-    if (s < kSlowScale) {
+    const Divisor d = divisor(s, m == 0.0f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rcodes[i] = encode_row<E5M2, true, DT>(v[i], s, inv);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rcodes[i] = encode_row<E5M2, false, DT>(v[i], s, inv);
-    }
+    for (int i = 0; i < 4; ++i)
+      rcodes[i] = d.slow ? encode_row<E5M2, true, DT>(v[i], d) : encode_row<E5M2, false, DT>(v[i], d);
     if (tid == 0) {
       if (ROWS) a.scales[rb * a.nbc + cb] = s;
       if (COLS) a.scales_t[cb * a.nbr + rb] = s;
@@ -141,15 +146,12 @@ __global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a
       if constexpr (BLOCK) {
         codes = rcodes[i];
       } else {
-        float m = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) m = amax2(m, v[i].get(c));
+        float m = v[i].amax();
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
         const float s = tile_scale<E5M2>(m, a.pow2);
-        const float inv = recip(s);
-        codes = s < kSlowScale ? encode_row<E5M2, true, DT>(v[i], s, inv)
-                               : encode_row<E5M2, false, DT>(v[i], s, inv);
+        const Divisor d = divisor(s, m == 0.0f);
+        codes = d.slow ? encode_row<E5M2, true, DT>(v[i], d) : encode_row<E5M2, false, DT>(v[i], d);
         s4[i] = s;
       }
       // (a row's 16-byte piece ends within the row's padding to 16 bytes)
@@ -178,30 +180,46 @@ __global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a
         sh_codes[word_at(c + 3, g)] = __byte_perm(AB, CD, 0x7632);
       }
     } else {
-      float m[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        m[c] = fabsf(v[0].get(c));
-#pragma unroll
-        for (int i = 1; i < 4; ++i) m[c] = amax2(m[c], v[i].get(c));
-      }
       // each step keeps half of the columns held: lane bit 3 columns 8-15 of
       // the 16, then lane bit 4 the upper four of those eight
-      float h[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float keep = (lane & 8) ? m[c + 8] : m[c];
-        const float give = (lane & 8) ? m[c] : m[c + 8];
-        h[c] = amax2(keep, __shfl_xor_sync(~0u, give, 8));
-      }
+      const bool hi8 = lane & 8, hi4 = lane & 16;
       float q[4];
+      if constexpr (DT == kFP32) {
+        float m[16], h[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float keep = (lane & 16) ? h[c + 4] : h[c];
-        const float give = (lane & 16) ? h[c] : h[c + 4];
-        q[c] = amax2(keep, __shfl_xor_sync(~0u, give, 16));
+        for (int c = 0; c < 16; ++c) {
+          m[c] = fabsf(v[0].get(c));
+#pragma unroll
+          for (int i = 1; i < 4; ++i) m[c] = amax2(m[c], v[i].get(c));
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          h[c] = amax2(hi8 ? m[c + 8] : m[c], __shfl_xor_sync(~0u, hi8 ? m[c] : m[c + 8], 8));
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          q[c] = amax2(hi4 ? h[c + 4] : h[c], __shfl_xor_sync(~0u, hi4 ? h[c] : h[c + 4], 16));
+      } else {
+        uint32_t m[8], h[4];   // pairs of columns
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          m[c] = v[0].w[c];
+#pragma unroll
+          for (int i = 1; i < 4; ++i) m[c] = amax_pair<DT>(m[c], v[i].w[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          h[c] = amax_pair<DT>(hi8 ? m[c + 4] : m[c], __shfl_xor_sync(~0u, hi8 ? m[c] : m[c + 4], 8));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          Vec<DT, 8> t;
+          t.w[0] = amax_pair<DT>(hi4 ? h[c + 2] : h[c],
+                                 __shfl_xor_sync(~0u, hi4 ? h[c] : h[c + 2], 16)) & 0x7fff7fffu;
+          q[2 * c] = t.get(0);
+          q[2 * c + 1] = t.get(1);
+        }
       }
-      const int c0 = sub * 16 + ((lane & 8) ? 8 : 0) + ((lane & 16) ? 4 : 0);
+      if (tid == 0) sh_slow = 0;
+      const int c0 = sub * 16 + (hi8 ? 8 : 0) + (hi4 ? 4 : 0);
       *reinterpret_cast<float4*>(&sh_red[warp][c0]) = make_float4(q[0], q[1], q[2], q[3]);
       __syncthreads();
       if (tid < 128) {
@@ -209,19 +227,19 @@ __global__ void __launch_bounds__(kThreads) quant128_kernel(const Quant128Args a
 #pragma unroll
         for (int w = 1; w < 8; ++w) mm = amax2(mm, sh_red[w][tid]);
         const float s = tile_scale<E5M2>(mm, a.pow2);
-        sh_s[tid] = s;
-        sh_inv[tid] = recip(s);
+        const Divisor d = divisor(s, mm == 0.0f);
+        sh_s[tid] = d.s;
+        sh_inv[tid] = d.inv;
+        sh_lift[tid] = d.slow ? kLift : 1.0f;
+        if (d.slow) sh_slow = 1;
         // (columns past the edge: zero tiles; ldst >= cols rounded up to 4)
         if (cb * 128 + tid < ((a.cols + 3) & ~int64_t(3))) a.scales_t[rb * a.ldst + cb * 128 + tid] = s;
       }
       __syncthreads();
-      bool slow = false;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) slow |= sh_s[sub * 16 + c] < kSlowScale;
-      if (slow)
-        encode_cols<E5M2, true, DT>(v, sh_s, sh_inv, g, sub, sh_codes);
+      if (sh_slow)
+        encode_cols<E5M2, true, DT>(v, sh_s, sh_inv, sh_lift, g, sub, sh_codes);
       else
-        encode_cols<E5M2, false, DT>(v, sh_s, sh_inv, g, sub, sh_codes);
+        encode_cols<E5M2, false, DT>(v, sh_s, sh_inv, sh_lift, g, sub, sh_codes);
     }
     __syncthreads();
     // eight lanes write a column's 128 codes; 32 columns at a time
@@ -242,16 +260,14 @@ cudaError_t launch_fmt(const Quant128Args& a, bool block, cudaStream_t st) {
   if (pieces > 0x7fffffff) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(pieces);
   const bool rows = a.codes != nullptr, cols = a.codes_t != nullptr;
-  if (block) {
-    if (rows && cols) quant128_kernel<DT, E5M2, true, true, true><<<grid, kThreads, 0, st>>>(a);
-    else if (rows) quant128_kernel<DT, E5M2, true, false, true><<<grid, kThreads, 0, st>>>(a);
-    else quant128_kernel<DT, E5M2, false, true, true><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (rows && cols) quant128_kernel<DT, E5M2, true, true, false><<<grid, kThreads, 0, st>>>(a);
-    else if (rows) quant128_kernel<DT, E5M2, true, false, false><<<grid, kThreads, 0, st>>>(a);
-    else quant128_kernel<DT, E5M2, false, true, false><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  const auto kern =
+      block ? (rows && cols ? quant128_kernel<DT, E5M2, true, true, true>
+               : rows       ? quant128_kernel<DT, E5M2, true, false, true>
+                            : quant128_kernel<DT, E5M2, false, true, true>)
+            : (rows && cols ? quant128_kernel<DT, E5M2, true, true, false>
+               : rows       ? quant128_kernel<DT, E5M2, true, false, false>
+                            : quant128_kernel<DT, E5M2, false, true, false>);
+  return launch_dependent(kern, dim3(grid), dim3(kThreads), 0, st, 1, a);
 }
 
 }  // namespace

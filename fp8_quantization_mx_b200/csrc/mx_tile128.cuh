@@ -20,13 +20,26 @@ namespace mxk {
 namespace t128 {
 
 constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126
-// Below this scale the remainder x - q s of div_scale may be subnormal for an
-// x that still rounds to a nonzero code; such tiles divide instead.
+// Below this scale the remainder q s - x of div2 may be subnormal for an x that
+// still rounds to a nonzero code; such tiles are divided 2^64 times larger.
 constexpr float kSlowScale = 8.2718061e-25f;    // 2^-80
+constexpr float kLift = 1.84467441e19f;         // 2^64
 
 template <bool E5M2>
 __device__ __forceinline__ constexpr float max_code() {
   return E5M2 ? 57344.0f : 448.0f;
+}
+
+// Largest magnitudes of two pairs of 16-bit floats, NaN kept (the sign bits of
+// the result are to be ignored).
+template <int DT>
+__device__ __forceinline__ uint32_t amax_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (DT == 0)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // max(|a|, |b|) that keeps a NaN (a >= 0 or NaN).
@@ -51,16 +64,31 @@ __device__ __forceinline__ float tile_scale(float amax, bool pow2) {
 
 __device__ __forceinline__ float recip(float s) { return __frcp_rn(s); }
 
-// x / s correctly rounded, given inv = 1 / s correctly rounded: a quotient
-// within one unit in the last place, corrected by its exact remainder
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990). Three multiply-adds per element where a division takes
-// about ten; the rounded quotient is what ties of the codes are decided on.
-template <bool SLOW>
-__device__ __forceinline__ float div_scale(float x, float s, float inv) {
-  if constexpr (SLOW) return __fdiv_rn(x, s);
-  const float q = x * inv;
-  return fmaf(-fmaf(q, s, -x), inv, q);   // (signs chosen so that -0 / s stays -0)
+// {x.x / s.x, x.y / s.y} correctly rounded, given inv = 1 / s correctly rounded:
+// a quotient within one unit in the last place, corrected by its exact
+// remainder (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990; the signs keep -0 / s = -0). Ties of the codes
+// are decided on the rounded quotient. Packed: 1.5 instructions per element
+// where a division takes about ten.
+__device__ __forceinline__ float2 div2(float2 x, float2 s, float2 inv) {
+  const float2 q = __fmul2_rn(x, inv);
+  const float2 r = __ffma2_rn(q, s, make_float2(-x.x, -x.y));
+  return __ffma2_rn(make_float2(-r.x, -r.y), inv, q);
+}
+
+// A tile's scale with what division by it needs.
+struct Divisor {
+  float s, inv;   // as div2 takes them (both lifted for a tiny scale)
+  bool slow;      // x is to be lifted too
+};
+
+__device__ __forceinline__ Divisor divisor(float s, bool zero) {
+  Divisor d{s, recip(s), s < kSlowScale && !zero};
+  if (d.slow) {
+    d.s *= kLift;
+    d.inv *= 1.0f / kLift;
+  }
+  return d;
 }
 
 // Two codes: lo in bits 0-7, hi in bits 8-15.
@@ -149,6 +177,23 @@ struct Vec {
       return (i & 1) ? __high2float(h) : __low2float(h);
     } else {
       return __uint_as_float(w[i]);
+    }
+  }
+  __device__ __forceinline__ float2 get2(int i) const { return make_float2(get(2 * i), get(2 * i + 1)); }
+  // The largest magnitude, NaN kept.
+  __device__ __forceinline__ float amax() const {
+    if constexpr (DT == kFP32) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = amax2(m, get(i));
+      return m;
+    } else {
+      uint32_t m = w[0];
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) m = amax_pair<DT>(m, w[i]);
+      Vec<DT, 8> t;   // (its first pair)
+      t.w[0] = m & 0x7fff7fffu;
+      return amax2(t.get(0), t.get(1));
     }
   }
   // Elements 2i and 2i + 1, each rounded to nearest even.

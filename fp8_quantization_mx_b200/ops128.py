@@ -26,16 +26,19 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NO_SWITCH = contextlib.nullcontext()
 
 
-def _up(n: int, to: int) -> int:
-    return (n + to - 1) // to * to
-
-
 def _on(device):
     """Makes ``device`` current, without the cost of a switch where it is."""
     return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+# The current stream's handle by device index, without building a Stream object
+# (2 us of a call that takes 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -74,23 +77,27 @@ def _contiguous(t, name: str, device, dtype, shape):
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _new_codes(rows: int, cols: int, device):
-    pitch = _up(cols, 16)
-    held = torch.empty(rows, pitch, dtype=torch.uint8, device=device)
-    return held if pitch == cols else held[:, :cols]
+    """A code matrix for the quantizers to write, and its row pitch."""
+    pitch = (cols + 15) // 16 * 16
+    held = torch.empty((rows, pitch), dtype=torch.uint8, device=device)
+    return (held if pitch == cols else held[:, :cols]), pitch
 
 
 def _new_scales(rows: int, cols: int, block: bool, device):
+    """Scales for the quantizers to write, and the pitch of tile scales."""
     nb = (cols + 127) // 128
     if block:
-        return torch.empty((rows + 127) // 128, nb, dtype=torch.float32, device=device)
-    return torch.empty(nb, _up(rows, 4), dtype=torch.float32, device=device).t()[:rows]
+        return torch.empty(((rows + 127) // 128, nb), dtype=torch.float32, device=device), 4
+    pitch = (rows + 3) // 4 * 4
+    held = torch.empty_strided((pitch, nb), (1, pitch), dtype=torch.float32, device=device)
+    return (held if pitch == rows else held[:rows]), pitch
 
 
 def _codes(t, name: str, device, rows=None, cols=None) -> int:
@@ -102,16 +109,20 @@ def _codes(t, name: str, device, rows=None, cols=None) -> int:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != torch.uint8:
         raise ValueError(f"{name} must be uint8, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or \
-            (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or \
+            (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, "
-                         f"{'cols' if cols is None else cols}], got {list(t.shape)}")
-    rows, cols = t.shape
-    need = _up(cols, 16)
+                         f"{'cols' if cols is None else cols}], got {list(shape)}")
+    rows, cols = shape
+    need = (cols + 15) // 16 * 16
     if rows == 0 or cols == 0:
         return need
-    pitch = t.stride(0) if rows > 1 else need
-    if (cols > 1 and t.stride(1) != 1) or pitch < need or pitch % 16:
+    stride = t.stride()
+    pitch = stride[0] if rows > 1 else need
+    if pitch == cols == need and stride[1] == 1:
+        return pitch   # whole rows end to end: nothing beyond them is read
+    if (cols > 1 and stride[1] != 1) or pitch < need or pitch % 16:
         raise ValueError(f"{name} must have contiguous rows a multiple of 16 bytes apart, at least "
                          f"{need}")
     if t.storage_offset() + (rows - 1) * pitch + need > t.untyped_storage().nbytes():
@@ -128,17 +139,20 @@ def _scales(t, name: str, device, rows: int, cols: int, block: bool) -> int:
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be float32, got {t.dtype}")
     shape = ((rows + 127) // 128 if block else rows, nb)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if block:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return 4
-    need = _up(rows, 4)
+    need = (rows + 3) // 4 * 4
     if rows == 0 or cols == 0:
         return need
-    pitch = t.stride(1) if nb > 1 else need
-    if (rows > 1 and t.stride(0) != 1) or pitch < need or pitch % 4:
+    stride = t.stride()
+    pitch = stride[1] if nb > 1 else need
+    if pitch == need == rows and stride[0] == 1:
+        return pitch
+    if (rows > 1 and stride[0] != 1) or pitch < need or pitch % 4:
         raise ValueError(f"{name} must be stored tile by tile (strides (1, pitch), pitch a multiple "
                          f"of 4 and at least {need}), as quantize128 returns them")
     if (t.storage_offset() + (nb - 1) * pitch + need) * 4 > t.untyped_storage().nbytes():
@@ -165,13 +179,17 @@ def quantize128(x: torch.Tensor, format: int = E4M3, block: bool = False, direct
     dev = x.device
     sides = (((rows, cols),) if direction != "cols" else ()) + \
             (((cols, rows),) if direction != "rows" else ())
+    args, given = [], out
     if out is None:
-        out = tuple(t for r, c in sides
-                    for t in (_new_codes(r, c, dev), _new_scales(r, c, block, dev)))
+        out = ()
+        for r, c in sides:
+            codes, ld = _new_codes(r, c, dev)
+            scales, lds = _new_scales(r, c, block, dev)
+            out += (codes, scales)
+            args += [codes.data_ptr(), ld, scales.data_ptr(), lds]
     elif len(out) != 2 * len(sides):
         raise ValueError(f"out must hold {2 * len(sides)} tensors")
-    args = []
-    for i, (r, c) in enumerate(sides):
+    for i, (r, c) in enumerate(sides if given is not None else ()):
         codes, scales = out[2 * i], out[2 * i + 1]
         ld = _codes(codes, f"out[{2 * i}]", dev, r, c)
         lds = _scales(scales, f"out[{2 * i + 1}]", dev, r, c, block)
@@ -206,7 +224,7 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
     h = y = None
     if residual is not None:
         _contiguous(residual, "residual", dev, dt, (rows, cols))
-        h = torch.empty(rows, cols, dtype=dt, device=dev) if h_out is None else h_out
+        h = torch.empty((rows, cols), dtype=dt, device=dev) if h_out is None else h_out
     elif h_out is not None:
         raise ValueError("h_out without a residual: h is x")
     if h_out is not None:
@@ -214,12 +232,14 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
     if return_y:
         y = torch.empty(rows, cols, dtype=dt, device=dev)
     if out is None:
-        out = (_new_codes(rows, cols, dev), _new_scales(rows, cols, False, dev))
+        codes, ld = _new_codes(rows, cols, dev)
+        scales, lds = _new_scales(rows, cols, False, dev)
     elif len(out) != 2:
         raise ValueError("out must be (codes, scales)")
-    codes, scales = out
-    ld = _codes(codes, "codes", dev, rows, cols)
-    lds = _scales(scales, "scales", dev, rows, cols, False)
+    else:
+        codes, scales = out
+        ld = _codes(codes, "codes", dev, rows, cols)
+        lds = _scales(scales, "scales", dev, rows, cols, False)
     with _on(dev):
         _c._check(_c.mx_rms_norm_quant128(
             x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), weight.data_ptr(),
@@ -249,8 +269,7 @@ def rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     gh = torch.empty_like(h) if out is None else out
     gw = torch.empty(cols, dtype=torch.float32, device=dev)
     with _on(dev):
-        work = torch.empty(max(0, _c.mx_rms_norm_bwd_workspace(rows, cols)), dtype=torch.uint8,
-                           device=dev)
+        work = torch.empty(_c.mx_rms_norm_bwd_workspace(rows, cols), dtype=torch.uint8, device=dev)
         _c._check(_c.mx_rms_norm_bwd(
             grad_y.data_ptr(), h.data_ptr(), weight.data_ptr(),
             None if grad_residual is None else grad_residual.data_ptr(), _DTYPES[dt], rows, cols, eps,
