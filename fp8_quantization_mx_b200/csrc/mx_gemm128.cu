@@ -774,33 +774,101 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
 
 }  // namespace
 
-Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms) {
-  (void)b_block;
-  Plan128 p{};
-  const int64_t nk = (K + 127) / 128;
-  p.swap = M <= 64;
-  p.bn = p.swap ? (M <= 16 ? 16 : M <= 32 ? 32 : 64) : N <= 64 ? 64 : N <= 128 ? 128 : 256;
-  const auto tiles = [&]() {
-    const int64_t P = p.swap ? N : M, Q = p.swap ? M : N;
-    return ((P + 127) / 128) * ((Q + p.bn - 1) / p.bn);
+// The cheapest cut by a model of the time: waves of clusters times the K-blocks
+// of a CTA times a K-block's time, plus what joining a split costs. Measured on
+// a B200 (us; a K-block of each tile in a full wave, one join per size):
+//   a tile that is finer than needed loses to its number of waves, one that is
+//   coarser leaves SMs idle: 128 x 8192 x 4096 takes 12.6 us in 64-wide tiles,
+//   13.9 in 128-wide ones on twice the CTAs per tile, 19.2 in pairs' tiles;
+//   512 x 8192 x 8192 takes 66 us in 64-wide tiles, 50 and 34.
+//   Clusters are not free to pack: 17 of 8 CTAs run as two waves (13.5 us, 9.5
+//   with clusters of 4), since a cluster stays within one of the GPU's SM groups.
+Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int clusters4,
+                     int clusters8) {
+  struct Cut {
+    int bn, swap;
+    double kb_block, kb_tile, tail;   // per K-block with block / tile weights, per wave
   };
-  if (!p.swap && p.bn == 256 && tiles() < sms) p.bn = 128;
-  p.split = 1;
-  while (p.split < 8 && tiles() * p.split * 2 <= sms && nk >= p.split * 4) p.split *= 2;
-  return p;
+  static constexpr Cut kCuts[] = {
+      {16, 1, 0.22, 0.22, 0.3}, {32, 1, 0.225, 0.225, 0.4}, {64, 1, 0.25, 0.25, 0.6},
+      {64, 0, 0.19, 0.25, 0.3}, {128, 0, 0.32, 0.55, 1.0},  {256, 0, 0.42, 0.80, 1.5}};
+  static constexpr double kJoin[] = {0.0, 0.5, 1.0, 1.3};
+  const int64_t nk = (K + 127) / 128;
+  Plan128 best{};
+  double best_t = 0.0;
+  for (const Cut& c : kCuts) {
+    const int64_t P = c.swap ? N : M, Q = c.swap ? M : N;
+    const int64_t rows = c.bn == 256 ? 256 : 128;
+    const int64_t tiles = ((P + rows - 1) / rows) * ((Q + c.bn - 1) / c.bn);
+    for (int i = 0; i < 4; ++i) {
+      const int split = 1 << i;
+      if (split > nk || (c.bn == 256 && split > 1)) break;
+      const int64_t slots = c.bn == 256 ? sms / 2 : i == 0 ? sms : i == 1 ? sms / 2
+                                                  : i == 2 ? clusters4 : clusters8;
+      if (slots < 1) break;
+      const int64_t waves = (tiles + slots - 1) / slots;
+      const double t = static_cast<double>(waves) *
+                           (static_cast<double>((nk + split - 1) / split) *
+                                (b_block ? c.kb_block : c.kb_tile) + c.tail) + kJoin[i];
+      if (best.bn == 0 || t < best_t) {
+        best = {c.bn, c.swap, split};
+        best_t = t;
+      }
+    }
+  }
+  return best;
 }
+
+namespace {
+
+// Clusters of 4 and of 8 CTAs (one per SM) that the device holds at once.
+cudaError_t device_clusters(int dev, int* c4, int* c8) {
+  static std::atomic<int> known[kMaxDevices];   // c4 | c8 << 16, 0 unknown
+  int v = known[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    using C = Cfg<128, false, false, false, 6>;
+    auto kern = gemm128_kernel<C>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(C::kSmem));
+    int n[2] = {0, 0};
+    for (int i = 0; e == cudaSuccess && i < 2; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = i ? 8 : 4;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(1024);
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kSmem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n[i], kern, &cfg);
+    }
+    if (e != cudaSuccess) return e;
+    v = n[0] | n[1] << 16;
+    known[dev].store(v, std::memory_order_relaxed);
+  }
+  *c4 = v & 0xffff;
+  *c8 = v >> 16;
+  return cudaSuccess;
+}
+
+}  // namespace
 
 cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st) {
   int dev = 0, sms = 0;
-  const cudaError_t e = device_sms(&dev, &sms);
+  cudaError_t e = device_sms(&dev, &sms);
+  int c4 = 0, c8 = 0;
+  if (e == cudaSuccess && !plan) e = device_clusters(dev, &c4, &c8);
   if (e != cudaSuccess) return e;
-  const Plan128 p = plan ? *plan : plan_gemm128(u.M, u.N, u.K, u.b_block, sms);
+  const Plan128 p = plan ? *plan : plan_gemm128(u.M, u.N, u.K, u.b_block, sms, c4, c8);
   Gemm128Args g{};
   g.d = static_cast<uint8_t*>(u.d);
   g.status = u.status;
   g.ldd = u.N;
   g.nk = static_cast<int>((u.K + 127) / 128);
-  g.split = p.split;
+  g.split = p.bn == 256 ? 1 : p.split;
   g.out_fp32 = u.out_fp32;
   g.vec = u.N * (u.out_fp32 ? 4 : 2) % 16 == 0;
   if (p.swap) {

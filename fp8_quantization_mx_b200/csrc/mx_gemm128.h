@@ -27,7 +27,9 @@ struct Plan128 {
   int bn, swap, split;
 };
 
-Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms);
+// sms, and how many clusters of 4 and of 8 one-per-SM CTAs run at once.
+Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int clusters4,
+                     int clusters8);
 
 // plan: NULL for plan_gemm128's choice on the current device.
 cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st);

@@ -81,132 +81,187 @@ __device__ __forceinline__ uint2 encode8(const float (&y)[8], const Divisor& d) 
                     enc4<E5M2>(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
-// One CTA per row, NV vectors of 8 elements per thread: the vectors of a tile
-// are 16 neighbouring lanes' (four shuffles give its largest magnitude).
-template <int DT, bool E5M2, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm128_kernel(const NormArgs a) {
+// The threads of a row: a whole CTA, or (WARP, rows of up to 1024 elements) one
+// of its eight warps, which needs no barrier. CTAs are as many as the SMs hold;
+// each takes every gridDim-th row (or eight), and the next row's loads are
+// issued before this row's sums, so that HBM is busy across them.
+template <bool WARP>
+struct RowThreads {
+  int tid, nt;
+  int64_t first, step;
+  __device__ RowThreads()
+      : tid(WARP ? threadIdx.x & 31 : threadIdx.x),
+        nt(WARP ? 32 : blockDim.x),
+        first(WARP ? blockIdx.x * int64_t(8) + (threadIdx.x >> 5) : blockIdx.x),
+        step(WARP ? gridDim.x * int64_t(8) : gridDim.x) {}
+  // Sums over the row's threads, the same in each (two buffers in turn: the
+  // next row's sums may start while a warp reads these).
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N], float (&red)[2][32 * N], int par) const {
+    if constexpr (WARP) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    } else {
+      block_sum(v, red[par]);
+    }
+  }
+};
+
+// NV vectors of 8 elements per thread: the vectors of a tile are 16
+// neighbouring lanes' (four shuffles give its largest magnitude).
+template <int DT, bool E5M2, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
+    norm128_kernel(const NormArgs a) {
   using T = typename Elem<DT>::T;
-  __shared__ float red[32];
-  const int tid = threadIdx.x, nt = blockDim.x;
+  __shared__ float red[2][32];
+  const RowThreads<WARP> rt;
   dependent_launch();
   dependent_wait();
-  const int64_t row = blockIdx.x;
   const int nvec = static_cast<int>(a.cols / 8);
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
-
-  Vec<DT, 8> xv[NV], rv[NV];
+  const int64_t pitch = (a.cols + 15) & ~int64_t(15);
+  Vec<DT, 8> xv[NV], rv[NV], wv[NV];
+  const auto load = [&](int64_t row, Vec<DT, 8>(&x)[NV], Vec<DT, 8>(&r)[NV]) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * nt;
-    xv[j].zero();
-    rv[j].zero();
-    if (i < nvec) {
-      xv[j].load(x + 8 * i);
-      if (res) rv[j].load(res + 8 * i);
+    for (int j = 0; j < NV; ++j) {
+      const int i = rt.tid + j * rt.nt;
+      x[j].zero();
+      r[j].zero();
+      if (i < nvec && row < a.rows) {
+        x[j].load(static_cast<const T*>(a.x) + row * a.ldx + 8 * i);
+        if (a.residual) r[j].load(static_cast<const T*>(a.residual) + row * a.cols + 8 * i);
+      }
     }
-  }
-  Vec<DT, 8> wv[NV];
-  float h[NV][8];
-  float ss[1] = {0.0f};
+  };
+  load(rt.first, xv, rv);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * nt;
+    const int i = rt.tid + j * rt.nt;
     wv[j].zero();
     if (i < nvec) wv[j].load(static_cast<const T*>(a.weight) + 8 * i);
-    float p = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[j][e] = xv[j].get(e) + rv[j].get(e);
-      p = fmaf(h[j][e], h[j][e], p);
-    }
-    ss[0] += p;
-    if (a.h && i < nvec) {
-      Vec<DT, 8> o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o.set2(e, h[j][2 * e], h[j][2 * e + 1]);
-      o.store(static_cast<T*>(a.h) + row * a.cols + 8 * i);
-    }
   }
-  block_sum(ss, red);
-  const float r = row_rstd(ss[0], a.cols, a.eps);
+  int par = 0;
+  for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
+    Vec<DT, 8> xn[NV], rn[NV];
+    load(row + rt.step, xn, rn);
+    float h[NV][8];
+    float ss[1] = {0.0f};
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * nt;
-    float y[8], m = 0.0f;
+    for (int j = 0; j < NV; ++j) {
+      const int i = rt.tid + j * rt.nt;
+      float p = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = h[j][e] * r * wv[j].get(e);
-      m = amax2(m, y[e]);
-    }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
-    const float s = tile_scale<E5M2>(m, a.pow2);
-    const uint2 c = encode8<E5M2>(y, divisor(s, m == 0.0f));
-    // codes up to the row's padding to 16 bytes (the vector past the last is 0)
-    if (8 * static_cast<int64_t>(i) < ((a.cols + 15) & ~int64_t(15)))
-      *reinterpret_cast<uint2*>(a.codes + row * a.ldc + 8 * i) = c;
-    if (i < nvec) {
-      if ((i & 15) == 0) a.scales[(i >> 4) * a.lds + row] = s;
-      if (a.y) {
+      for (int e = 0; e < 8; ++e) {
+        h[j][e] = xv[j].get(e) + rv[j].get(e);
+        p = fmaf(h[j][e], h[j][e], p);
+      }
+      ss[0] += p;
+      if (a.h && i < nvec) {
         Vec<DT, 8> o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.set2(e, y[2 * e], y[2 * e + 1]);
-        o.store(static_cast<T*>(a.y) + row * a.cols + 8 * i);
+        for (int e = 0; e < 4; ++e) o.set2(e, h[j][2 * e], h[j][2 * e + 1]);
+        o.store(static_cast<T*>(a.h) + row * a.cols + 8 * i);
       }
+    }
+    rt.sum(ss, red, par);
+    const float r = row_rstd(ss[0], a.cols, a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = rt.tid + j * rt.nt;
+      float y[8], m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = h[j][e] * r * wv[j].get(e);
+        m = amax2(m, y[e]);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
+      const float s = tile_scale<E5M2>(m, a.pow2);
+      const uint2 c = encode8<E5M2>(y, divisor(s, m == 0.0f));
+      // codes up to the row's padding to 16 bytes (the vector past the last is 0)
+      if (8 * static_cast<int64_t>(i) < pitch)
+        *reinterpret_cast<uint2*>(a.codes + row * a.ldc + 8 * i) = c;
+      if (i < nvec) {
+        if ((i & 15) == 0) a.scales[(i >> 4) * a.lds + row] = s;
+        if (a.y) {
+          Vec<DT, 8> o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.set2(e, y[2 * e], y[2 * e + 1]);
+          o.store(static_cast<T*>(a.y) + row * a.cols + 8 * i);
+        }
+      }
+      xv[j] = xn[j];
+      rv[j] = rn[j];
     }
   }
 }
 
-// Any number of columns at any alignment: the row is read twice (the second
-// time mostly from cache); one warp per tile, 4 elements per lane.
-template <int DT, bool E5M2>
+// Any number of columns at any alignment: one CTA per row, element tid + 256 j
+// in thread tid. Up to 256 NJ columns stay in registers; beyond, the row is
+// read again (mostly from cache).
+template <int DT, bool E5M2, int NJ>
 __global__ void __launch_bounds__(256) norm128_any_kernel(const NormArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   __shared__ float red[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float sh_max[NJ][8];
+  __shared__ Divisor sh_div[2 * NJ];
   dependent_launch();
   dependent_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
   const T* w = static_cast<const T*>(a.weight);
-  float ss[1] = {0.0f};
-  for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-    const float v = E::to_float(x[c]) + (res ? E::to_float(res[c]) : 0.0f);
+  const auto h_at = [&](int64_t c) {
+    return c < a.cols ? E::to_float(x[c]) + (res ? E::to_float(res[c]) : 0.0f) : 0.0f;
+  };
+  float h[NJ], ss[1] = {0.0f};
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    h[j] = h_at(tid + 256 * j);
+    ss[0] = fmaf(h[j], h[j], ss[0]);
+  }
+  for (int64_t c = tid + 256 * NJ; c < a.cols; c += 256) {
+    const float v = h_at(c);
     ss[0] = fmaf(v, v, ss[0]);
   }
   block_sum(ss, red);
   const float r = row_rstd(ss[0], a.cols, a.eps);
   const int64_t pitch = (a.cols + 15) & ~int64_t(15);
-  for (int64_t t = warp; t < (a.cols + 127) / 128; t += 8) {
-    const int64_t c0 = t * 128 + 4 * lane;
-    float h[4], y[4], m = 0.0f;
+  for (int64_t c0 = 0; c0 < a.cols; c0 += 256 * NJ) {
+    float y[NJ];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      h[e] = y[e] = 0.0f;
-      if (c0 + e < a.cols) {
-        h[e] = E::to_float(x[c0 + e]) + (res ? E::to_float(res[c0 + e]) : 0.0f);
-        y[e] = h[e] * r * E::to_float(w[c0 + e]);
-      }
-      m = amax2(m, y[e]);
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = c0 + tid + 256 * j;
+      if (c0 > 0) h[j] = h_at(c);
+      y[j] = c < a.cols ? h[j] * r * E::to_float(w[c]) : 0.0f;
+      float m = fabsf(y[j]);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
+      if (lane == 0) sh_max[j][warp] = m;
     }
+    __syncthreads();
+    if (tid < 2 * NJ) {   // a tile is four warps' elements
+      const float* p = &sh_max[tid >> 1][(tid & 1) * 4];
+      const float m = amax2(amax2(p[0], p[1]), amax2(p[2], p[3]));
+      const float s = tile_scale<E5M2>(m, a.pow2);
+      sh_div[tid] = divisor(s, m == 0.0f);
+      const int64_t t = c0 / 128 + tid;
+      if (t * 128 < a.cols) a.scales[t * a.lds + row] = s;
+    }
+    __syncthreads();
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
-    const float s = tile_scale<E5M2>(m, a.pow2);
-    float q[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = __fdiv_rn(y[e], s);
-    if (c0 < pitch)
-      *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + c0) = enc4<E5M2>(q[0], q[1], q[2], q[3]);
-    if (lane == 0) a.scales[t * a.lds + row] = s;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c0 + e < a.cols) {
-        if (a.h) static_cast<T*>(a.h)[row * a.cols + c0 + e] = E::from_float(h[e]);
-        if (a.y) static_cast<T*>(a.y)[row * a.cols + c0 + e] = E::from_float(y[e]);
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = c0 + tid + 256 * j;
+      const Divisor d = sh_div[2 * j + (warp >> 2)];
+      const float v = d.slow ? y[j] * kLift : y[j];
+      const float2 q = div2(make_float2(v, 0.0f), make_float2(d.s, d.s), make_float2(d.inv, d.inv));
+      if (c < pitch) a.codes[row * a.ldc + c] = static_cast<uint8_t>(enc2<E5M2>(q.x, 0.0f));
+      if (c < a.cols) {
+        if (a.h) static_cast<T*>(a.h)[row * a.cols + c] = E::from_float(h[j]);
+        if (a.y) static_cast<T*>(a.y)[row * a.cols + c] = E::from_float(y[j]);
       }
+    }
   }
 }
 
@@ -223,38 +278,42 @@ struct NormBwdArgs {
   float eps;
 };
 
-// CTA b takes rows b, b + gridDim.x, ...; a thread keeps its columns' share of
-// gw in registers (shared memory with four vectors a thread) over all of them. The next row's loads are issued before
-// this row's sums, so that HBM is busy across the barrier (not with four
-// vectors a thread, whose registers the next row would not fit).
-template <int DT, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_bwd_kernel(const NormBwdArgs a) {
+// A thread keeps its columns' share of gw in registers (shared memory with four
+// vectors a thread in a CTA) over all its rows; WARP: the CTA's eight warps add
+// theirs up at the end. (With four vectors a thread the next row's loads do not
+// fit the registers and wait.)
+template <int DT, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WARP && NV == 2 ? 2 : 1)
+    norm_bwd_kernel(const NormBwdArgs a) {
   using T = typename Elem<DT>::T;
+  constexpr bool kAhead = NV <= 2;
+  constexpr bool kShared = NV > 2 && !WARP;    // gw: [NV][2][threads] of float4
   __shared__ float red[2][64];
-  const int tid = threadIdx.x, nt = blockDim.x;
+  extern __shared__ __align__(16) float4 sh_gw[];
+  const RowThreads<WARP> rt;
+  const int tid = rt.tid, nt = rt.nt;
   dependent_launch();
   dependent_wait();
   const int nvec = static_cast<int>(a.cols / 8);
-  const T* gy = static_cast<const T*>(a.gy);
-  const T* hh = static_cast<const T*>(a.h);
-  constexpr bool kAhead = NV <= 2;
-  constexpr bool kShared = NV > 2;    // gw in shared memory: [NV][2][threads] of float4
-  extern __shared__ __align__(16) float4 sh_gw[];
   float gw[kShared ? 1 : NV][8];
   Vec<DT, 8> wv[NV], gv[NV], hv[NV];
+  const auto load = [&](int64_t row, Vec<DT, 8>(&g)[NV], Vec<DT, 8>(&h)[NV]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * nt;
+      g[j].zero();
+      h[j].zero();
+      if (i < nvec && row < a.rows) {
+        g[j].load(static_cast<const T*>(a.gy) + row * a.cols + 8 * i);
+        h[j].load(static_cast<const T*>(a.h) + row * a.cols + 8 * i);
+      }
+    }
+  };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = tid + j * nt;
     wv[j].zero();
-    gv[j].zero();
-    hv[j].zero();
-    if (i < nvec) {
-      wv[j].load(static_cast<const T*>(a.weight) + 8 * i);
-      if (kAhead) {
-        gv[j].load(gy + blockIdx.x * a.cols + 8 * i);
-        hv[j].load(hh + blockIdx.x * a.cols + 8 * i);
-      }
-    }
+    if (i < nvec) wv[j].load(static_cast<const T*>(a.weight) + 8 * i);
     if constexpr (kShared) {
       sh_gw[(2 * j) * nt + tid] = sh_gw[(2 * j + 1) * nt + tid] = make_float4(0, 0, 0, 0);
     } else {
@@ -262,26 +321,17 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_bwd_kernel(const Nor
       for (int e = 0; e < 8; ++e) gw[j][e] = 0.0f;
     }
   }
+  if (kAhead) load(rt.first, gv, hv);
   int par = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
-    const int64_t next = row + gridDim.x;
+  for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     Vec<DT, 8> gn[NV], hn[NV], rv[NV];
+    if (kAhead) load(row + rt.step, gn, hn);
+    else load(row, gv, hv);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * nt;
-      gn[j].zero();
-      hn[j].zero();
       rv[j].zero();
-      if (i < nvec) {
-        if (a.gres) rv[j].load(static_cast<const T*>(a.gres) + row * a.cols + 8 * i);
-        if (!kAhead) {
-          gv[j].load(gy + row * a.cols + 8 * i);
-          hv[j].load(hh + row * a.cols + 8 * i);
-        } else if (next < a.rows) {
-          gn[j].load(gy + next * a.cols + 8 * i);
-          hn[j].load(hh + next * a.cols + 8 * i);
-        }
-      }
+      if (a.gres && i < nvec) rv[j].load(static_cast<const T*>(a.gres) + row * a.cols + 8 * i);
     }
     float s[2] = {0.0f, 0.0f};   // sum h^2, sum gy w h
 #pragma unroll
@@ -292,8 +342,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_bwd_kernel(const Nor
         s[0] = fmaf(h, h, s[0]);
         s[1] = fmaf(gv[j].get(e) * wv[j].get(e), h, s[1]);
       }
-    // (two buffers: the next row's sums may start while a warp reads these)
-    block_sum(s, red[par]);
+    rt.sum(s, red, par);
     const float r = row_rstd(s[0], a.cols, a.eps);
     const float c = __fdiv_rn(s[1] * r, static_cast<float>(a.cols));
 #pragma unroll
@@ -328,61 +377,109 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512) norm_bwd_kernel(const Nor
       }
     }
   }
+  float* part = a.part + blockIdx.x * a.cols;
+  if constexpr (WARP) {
+    // the warps' shares, vector by vector: [8 warps][32 lanes][8]
+    __shared__ __align__(16) float sh_part[8][32 * 8];
+    const int warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tid + j * nt;
-    if (i < nvec) {
-      float4* p = reinterpret_cast<float4*>(a.part + blockIdx.x * a.cols + 8 * i);
-      if constexpr (kShared) {
-        p[0] = sh_gw[(2 * j) * nt + tid];
-        p[1] = sh_gw[(2 * j + 1) * nt + tid];
-      } else {
-        p[0] = make_float4(gw[j][0], gw[j][1], gw[j][2], gw[j][3]);
-        p[1] = make_float4(gw[j][4], gw[j][5], gw[j][6], gw[j][7]);
+    for (int j = 0; j < NV; ++j) {
+      if (j) __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sh_part[warp][tid * 8 + e] = gw[j][e];
+      __syncthreads();
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) sum += sh_part[w][threadIdx.x];
+      const int c = j * 256 + threadIdx.x;
+      if (c < a.cols) part[c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * nt;
+      if (i < nvec) {
+        float4* p = reinterpret_cast<float4*>(part + 8 * i);
+        if constexpr (kShared) {
+          p[0] = sh_gw[(2 * j) * nt + tid];
+          p[1] = sh_gw[(2 * j + 1) * nt + tid];
+        } else {
+          p[0] = make_float4(gw[j][0], gw[j][1], gw[j][2], gw[j][3]);
+          p[1] = make_float4(gw[j][4], gw[j][5], gw[j][6], gw[j][7]);
+        }
       }
     }
   }
 }
 
-// Any number of columns at any alignment: each thread adds to its own columns
-// of the CTA's share of gw in memory.
-template <int DT>
-__global__ void __launch_bounds__(256) norm_bwd_any_kernel(const NormBwdArgs a) {
+// Any number of columns at any alignment, element tid + 256 j in thread tid: up
+// to 256 NJ columns in registers; beyond, a row is read twice and a thread adds
+// to its columns of the CTA's share of gw in memory.
+template <int DT, int NJ>
+__global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(const NormBwdArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   __shared__ float red[2][64];
   dependent_launch();
   dependent_wait();
+  const int tid = threadIdx.x;
   const T* w = static_cast<const T*>(a.weight);
   float* part = a.part + blockIdx.x * a.cols;
+  float gw[NJ], wv[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    gw[j] = 0.0f;
+    wv[j] = tid + 256 * j < a.cols ? E::to_float(w[tid + 256 * j]) : 0.0f;
+  }
   int par = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
     const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
     const T* hh = static_cast<const T*>(a.h) + row * a.cols;
     const T* gres = a.gres ? static_cast<const T*>(a.gres) + row * a.cols : nullptr;
-    float s[2] = {0.0f, 0.0f};
-    for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-      const float h = E::to_float(hh[c]);
-      s[0] = fmaf(h, h, s[0]);
-      s[1] = fmaf(E::to_float(gy[c]) * E::to_float(w[c]), h, s[1]);
+    T* gh = static_cast<T*>(a.gh) + row * a.cols;
+    float g[NJ], h[NJ], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = tid + 256 * j;
+      g[j] = c < a.cols ? E::to_float(gy[c]) : 0.0f;
+      h[j] = c < a.cols ? E::to_float(hh[c]) : 0.0f;
+      s[0] = fmaf(h[j], h[j], s[0]);
+      s[1] = fmaf(g[j] * wv[j], h[j], s[1]);
+    }
+    for (int64_t c = tid + 256 * NJ; c < a.cols; c += 256) {
+      const float v = E::to_float(hh[c]);
+      s[0] = fmaf(v, v, s[0]);
+      s[1] = fmaf(E::to_float(gy[c]) * E::to_float(w[c]), v, s[1]);
     }
     block_sum(s, red[par]);
     const float r = row_rstd(s[0], a.cols, a.eps);
     const float m = __fdiv_rn(s[1] * r, static_cast<float>(a.cols));
-    for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-      const float n = E::to_float(hh[c]) * r, g = E::to_float(gy[c]);
-      part[c] = fmaf(g, n, row == blockIdx.x ? 0.0f : part[c]);
-      static_cast<T*>(a.gh)[row * a.cols + c] = E::from_float(
-          fmaf(r, fmaf(-n, m, g * E::to_float(w[c])), gres ? E::to_float(gres[c]) : 0.0f));
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = tid + 256 * j;
+      const float n = h[j] * r;
+      gw[j] = fmaf(g[j], n, gw[j]);
+      if (c < a.cols)
+        gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), gres ? E::to_float(gres[c]) : 0.0f));
+    }
+    for (int64_t c = tid + 256 * NJ; c < a.cols; c += 256) {
+      const float n = E::to_float(hh[c]) * r, v = E::to_float(gy[c]);
+      part[c] = fmaf(v, n, row == blockIdx.x ? 0.0f : part[c]);
+      gh[c] = E::from_float(
+          fmaf(r, fmaf(-n, m, v * E::to_float(w[c])), gres ? E::to_float(gres[c]) : 0.0f));
     }
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    if (tid + 256 * j < a.cols) part[tid + 256 * j] = gw[j];
 }
 
 // gw[c] = sum of the CTAs' shares, in an order that depends on their number
-// alone: 8 warps take every eighth share of 32 columns, then add up.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, int nparts,
-                                                           int64_t cols, float* gw) {
-  __shared__ float red[8][32];
+// alone: 32 warps take every 32nd share of 32 columns, then add up. (Latency:
+// with 8 warps the sum of 444 shares took 4 us.)
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int nparts,
+                                                            int64_t cols, float* gw) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   dependent_launch();
   dependent_wait();
@@ -390,73 +487,101 @@ __global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, in
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = warp; p < nparts; p += 8) s += part[p * cols + c];
+    for (int p = warp; p < nparts; p += 32) s += part[p * cols + c];
   }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    gw[c] = s;
-  }
+  // warp w adds up column w
+  s = warp_sum(red[lane][warp]);
+  const int64_t o = blockIdx.x * int64_t(32) + warp;
+  if (lane == 0 && o < cols) gw[o] = s;
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Vectors of 8 per thread and threads per row: one up to 2048 columns (256
-// threads), two up to 8192 and four up to 16384 (512 threads; beyond, the
-// kernel for any size).
+// How a row of nvec vectors is spread: up to 1024 elements one warp (one, two
+// or four vectors a lane), up to 2048 a CTA with one vector a thread, up to
+// 8192 two and up to 16384 four (512 threads at most); beyond, the kernel for
+// any size.
 constexpr int64_t kMaxVecCols = 16384;
-int vectors(int64_t nvec) { return nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4; }
-unsigned threads(int64_t nvec, int nv) {
-  return static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32);
+struct Shape {
+  bool warp;
+  int nv;
+  unsigned nt;
+};
+Shape shape_of(int64_t nvec) {
+  if (nvec <= 128) return {true, nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 256};
+  const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  return {false, nv, static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)};
+}
+
+// CTAs for `rows` rows with at most `threads` threads on an SM (what the
+// registers of the kernels' launch bounds allow: more CTAs than the SMs hold
+// would run as a second wave).
+int64_t grid_for(const Shape& s, int64_t rows, int sms, int threads) {
+  const int per_sm = threads / static_cast<int>(s.nt);
+  const int64_t most = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
+  const int64_t need = s.warp ? (rows + 7) / 8 : rows;
+  return need < most ? need : most;
 }
 
 template <int DT, bool E5M2>
-cudaError_t launch_norm(const NormArgs& a, bool vec, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.rows));
-  if (!vec) return launch_dependent(norm128_any_kernel<DT, E5M2>, grid, dim3(256), 0, st, 1, a);
-  const int64_t nvec = (a.cols + 15) / 16 * 2;   // with the codes' padding
-  const int nv = vectors(nvec);
-  const auto kern = nv == 1   ? norm128_kernel<DT, E5M2, 1>
-                    : nv == 2 ? norm128_kernel<DT, E5M2, 2>
-                              : norm128_kernel<DT, E5M2, 4>;
-  return launch_dependent(kern, grid, dim3(threads(nvec, nv)), 0, st, 1, a);
+cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
+  if (!vec) {
+    const auto kern = a.cols <= 1024   ? norm128_any_kernel<DT, E5M2, 4>
+                      : a.cols <= 2048 ? norm128_any_kernel<DT, E5M2, 8>
+                                       : norm128_any_kernel<DT, E5M2, 16>;
+    return launch_dependent(kern, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, st, 1, a);
+  }
+  const Shape s = shape_of((a.cols + 15) / 16 * 2);   // with the codes' padding
+  const auto kern = s.warp ? (s.nv == 1   ? norm128_kernel<DT, E5M2, 1, true>
+                              : s.nv == 2 ? norm128_kernel<DT, E5M2, 2, true>
+                                          : norm128_kernel<DT, E5M2, 4, true>)
+                           : (s.nv == 1   ? norm128_kernel<DT, E5M2, 1, false>
+                              : s.nv == 2 ? norm128_kernel<DT, E5M2, 2, false>
+                                          : norm128_kernel<DT, E5M2, 4, false>);
+  const int64_t grid = grid_for(s, a.rows, sms, s.nv == 1 ? 1024 : s.nv == 2 ? 704 : 512);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), 0, st, 1, a);
 }
 
-// CTAs: as many as the SMs hold at once (registers: 768 threads with one
-// vector each, else 512), the general kernel's 256-thread CTAs two per SM;
-// never more than rows or shares.
 template <int DT>
 cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaStream_t st) {
-  int64_t most = 2 * sms;
-  if (vec) {
-    const int nv = vectors(a.cols / 8);
-    const int per_sm = (nv == 1 ? 768 : 512) / static_cast<int>(threads(a.cols / 8, nv));
-    most = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
-  }
-  if (most > kNormParts) most = kNormParts;
-  const int grid = static_cast<int>(a.rows < most ? a.rows : most);
+  const Shape s = shape_of(a.cols / 8);
+  // (the kernels for any size: 256 threads, four CTAs per SM up to 2048 columns)
+  const int64_t any = (a.cols <= 2048 ? 4 : 2) * sms;
+  int64_t grid = vec ? grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512)
+                     : (a.rows < any ? a.rows : any);
+  if (grid > kNormParts) grid = kNormParts;
   cudaError_t e;
   if (!vec) {
-    e = launch_dependent(norm_bwd_any_kernel<DT>, dim3(grid), dim3(256), 0, st, 1, a);
+    const auto kern = a.cols <= 1024   ? norm_bwd_any_kernel<DT, 4>
+                      : a.cols <= 2048 ? norm_bwd_any_kernel<DT, 8>
+                                       : norm_bwd_any_kernel<DT, 16>;
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, 1, a);
   } else {
-    const int64_t nvec = a.cols / 8;
-    const int nv = vectors(nvec);
-    const unsigned nt = threads(nvec, nv);
-    const auto kern = nv == 1   ? norm_bwd_kernel<DT, 1>
-                      : nv == 2 ? norm_bwd_kernel<DT, 2>
-                                : norm_bwd_kernel<DT, 4>;
-    const size_t smem = nv == 4 ? nt * size_t(4 * 8 * 4) : 0;   // up to 64 KiB
+    const auto kern = s.warp ? (s.nv == 1   ? norm_bwd_kernel<DT, 1, true>
+                                : s.nv == 2 ? norm_bwd_kernel<DT, 2, true>
+                                            : norm_bwd_kernel<DT, 4, true>)
+                             : (s.nv == 1   ? norm_bwd_kernel<DT, 1, false>
+                                : s.nv == 2 ? norm_bwd_kernel<DT, 2, false>
+                                            : norm_bwd_kernel<DT, 4, false>);
+    const size_t smem = !s.warp && s.nv == 4 ? s.nt * size_t(4 * 8 * 4) : 0;   // up to 64 KiB
     if (smem) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 8 * 4);
       if (e != cudaSuccess) return e;
     }
-    e = launch_dependent(kern, dim3(grid), dim3(nt), smem, st, 1, a);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), smem, st, 1, a);
   }
   if (e != cudaSuccess) return e;
   return launch_dependent(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)),
-                          dim3(256), 0, st, 1, a.part, grid, a.cols, gw);
+                          dim3(1024), 0, st, 1, static_cast<const float*>(a.part),
+                          static_cast<int>(grid), a.cols, gw);
+}
+
+cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
 }  // namespace
@@ -484,13 +609,16 @@ cudaError_t launch_norm128(const void* x, int64_t ldx, const void* residual, con
   const bool vec = cols % 8 == 0 && cols <= kMaxVecCols && aligned16(x) && aligned16(residual) &&
                    aligned16(weight) && aligned16(h) && aligned16(y) &&
                    (rows == 1 || ldx * bytes % 16 == 0);
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
   switch (dtype * 2 + (e5m2 ? 1 : 0)) {
-    case 0: return launch_norm<kBF16, false>(a, vec, st);
-    case 1: return launch_norm<kBF16, true>(a, vec, st);
-    case 2: return launch_norm<kFP16, false>(a, vec, st);
-    case 3: return launch_norm<kFP16, true>(a, vec, st);
-    case 4: return launch_norm<kFP32, false>(a, vec, st);
-    default: return launch_norm<kFP32, true>(a, vec, st);
+    case 0: return launch_norm<kBF16, false>(a, vec, sms, st);
+    case 1: return launch_norm<kBF16, true>(a, vec, sms, st);
+    case 2: return launch_norm<kFP16, false>(a, vec, sms, st);
+    case 3: return launch_norm<kFP16, true>(a, vec, sms, st);
+    case 4: return launch_norm<kFP32, false>(a, vec, sms, st);
+    default: return launch_norm<kFP32, true>(a, vec, sms, st);
   }
 }
 
@@ -509,9 +637,8 @@ cudaError_t launch_norm_bwd(const void* gy, const void* h, const void* weight, c
   a.eps = eps;
   const bool vec = cols % 8 == 0 && cols <= kMaxVecCols && aligned16(gy) && aligned16(h) &&
                    aligned16(weight) && aligned16(gres) && aligned16(gh) && aligned16(part);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   switch (dtype) {
     case kBF16: return launch_bwd<kBF16>(a, vec, sms, gw, st);
