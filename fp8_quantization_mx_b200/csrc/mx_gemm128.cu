@@ -605,17 +605,29 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ok &= tc::mbar_wait(sm.done(h, st.slot), st.par, sm.abort_flag, g.status, kStatusSums);
         __syncwarp();
         tc::tc_fence_after();
-        constexpr int kLd = C::kCols < 32 ? 16 : 32;   // columns per load, two in flight
+        // Columns per load, two loads in flight. Column scales come a load ahead
+        // too (read where they are used, their latency took 280 ns per K-block).
+        constexpr int kLd = C::QCOL || C::kCols < 32 ? 16 : 32;
         const uint32_t taddr = lane_base + tb.slot * C::kUnitN;
         uint32_t r[2][kLd];
+        float4 f[2][C::QCOL ? kLd / 4 : 1];
+        const float4* qv = reinterpret_cast<const float4*>(col_scale + slot + at * C::BN);
         tc::tmem_ld_start(taddr, r[0]);
+        if constexpr (C::QCOL)
+#pragma unroll
+          for (int i = 0; i < kLd / 4; ++i) f[0][i] = qv[i];
         tc::tmem_ld_wait(r[0]);
 #pragma unroll
         for (int c0 = 0; c0 < C::kCols; c0 += kLd) {
-          uint32_t(&now)[kLd] = r[(c0 / kLd) & 1];
-          uint32_t(&next)[kLd] = r[(c0 / kLd + 1) & 1];
+          constexpr int kMask = 1;
+          uint32_t(&now)[kLd] = r[(c0 / kLd) & kMask];
+          uint32_t(&next)[kLd] = r[(c0 / kLd + 1) & kMask];
           if (c0 + kLd < C::kCols) {
             tc::tmem_ld_start(taddr + c0 + kLd, next);
+            if constexpr (C::QCOL)
+#pragma unroll
+              for (int i = 0; i < kLd / 4; ++i)
+                f[(c0 / kLd + 1) & kMask][i] = qv[(c0 + kLd) / 4 + i];
           } else {
             // the accumulator has been read
             tc::tc_fence_before();
@@ -625,16 +637,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               else tc::mbar_arrive_relaxed(free0 + 8 * tb.slot);
             }
           }
-          const float4* qv = reinterpret_cast<const float4*>(col_scale + slot + at * C::BN + c0);
 #pragma unroll
           for (int i = 0; i < kLd; i += 4) {
-            float4 f = make_float4(s, s, s, s);
+            float4 q = make_float4(s, s, s, s);
             if constexpr (C::QCOL) {
-              f = qv[i / 4];
-              f.x *= s, f.y *= s, f.z *= s, f.w *= s;
+              const float4 v = f[(c0 / kLd) & kMask][i / 4];
+              const float2 lo = __fmul2_rn(make_float2(v.x, v.y), make_float2(s, s));
+              const float2 hi = __fmul2_rn(make_float2(v.z, v.w), make_float2(s, s));
+              q = make_float4(lo.x, lo.y, hi.x, hi.y);
             }
-            fma2(acc[c0 + i], acc[c0 + i + 1], f.x, f.y, now[i], now[i + 1]);
-            fma2(acc[c0 + i + 2], acc[c0 + i + 3], f.z, f.w, now[i + 2], now[i + 3]);
+            fma2(acc[c0 + i], acc[c0 + i + 1], q.x, q.y, now[i], now[i + 1]);
+            fma2(acc[c0 + i + 2], acc[c0 + i + 3], q.z, q.w, now[i + 2], now[i + 3]);
           }
           if (c0 + kLd < C::kCols) tc::tmem_ld_wait(next);
         }
