@@ -1,4 +1,5 @@
-"""Builds libmx.so in-tree with nvcc for sm_100a (cross-compiles without a GPU).
+"""Builds libmx.so in-tree with nvcc for sm_100a (cross-compiles without a GPU),
+and the torch binding's small extension module with g++.
 
     python -m fp8_quantization_mx_b200.build [--force] [--verbose]
 
@@ -39,6 +40,39 @@ def nvcc() -> str:
 
 STAMP = LIB + ".srchash"
 
+# The C++ marshalling of the torch binding's 128-element calls: an extension
+# module against the torch it will run with.
+FAST = os.path.join(PKG, "_fast128.so")
+FAST_SRC = os.path.join(CSRC, "mx_fast128.cpp")
+
+
+def build_fast(force: bool = False) -> str:
+    """Builds _fast128.so unless the one in place was built from this source,
+    torch and Python."""
+    import sysconfig
+
+    import torch
+    with open(FAST_SRC, "rb") as f:
+        h = hashlib.sha256(f.read())
+    h.update(f"{torch.__version__} {sys.version}".encode())
+    want, stamp = h.hexdigest(), FAST + ".srchash"
+    if not force and os.path.exists(FAST) and _stamp(stamp) == want:
+        return FAST
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    inc = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(troot, "lib")
+    abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+                    *(f"-I{d}" for d in inc), FAST_SRC, "-o", FAST + ".tmp", f"-L{lib}",
+                    "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], check=True)
+    os.replace(FAST + ".tmp", FAST)
+    with open(stamp + ".tmp", "w") as f:
+        f.write(want + "\n")
+    os.replace(stamp + ".tmp", stamp)
+    return FAST
+
 
 def source_hash(extra=None) -> str:
     """SHA-256 over every source, header and flag the library is built from."""
@@ -53,9 +87,9 @@ def source_hash(extra=None) -> str:
     return h.hexdigest()
 
 
-def _stamp() -> str:
+def _stamp(path: str = STAMP) -> str:
     try:
-        with open(STAMP) as f:
+        with open(path) as f:
             return f.read().strip()
     except OSError:
         return ""
@@ -64,7 +98,9 @@ def _stamp() -> str:
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     """Builds libmx.so unless the one in place was built from these exact
     sources and flags (its recorded source hash matches); file times are not
-    trusted, so a stale library is always rebuilt."""
+    trusted, so a stale library is always rebuilt. The torch binding's
+    extension module is kept up to date beside it."""
+    build_fast(force)
     want = source_hash(extra)
     if not force and not verbose and os.path.exists(LIB) and _stamp() == want:
         return LIB

@@ -15,6 +15,7 @@ stored tile-major (strides ``(1, pitch)``), or per 128 x 128 block, contiguous
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -23,12 +24,41 @@ import fp8_quantization_mx_b200 as _c
 from . import BLOCK128, E4M3, E5M2, POW2_SCALES
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_DIRECTIONS = {"rows": 1, "cols": 2, "both": 3}
 _NO_SWITCH = contextlib.nullcontext()
 
 
 def _on(device):
     """Makes ``device`` current, without the cost of a switch where it is."""
     return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+# Calls with nothing unusual about them go through a C++ module that makes the
+# same checks, tensors and C calls (csrc/mx_fast128.cpp); it leaves every other
+# call to the code below. None until first used, False where it was not built.
+_fast = None
+
+
+def _bind_fast():
+    global _fast
+    lib = _c.load_library()
+    try:
+        from . import _fast128
+    except ModuleNotFoundError:
+        _fast = False
+        return False
+    _fast128.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.mx_quantize128, lib.mx_rms_norm_quant128, lib.mx_rms_norm_bwd,
+        lib.mx_rms_norm_bwd_workspace, lib.mx_gemm128)))
+    _fast = _fast128
+    return _fast
+
+
+def _made(result, where: str) -> bool:
+    """Whether the C++ module made the call (raises if the library refused it)."""
+    if type(result) is int:
+        _c._check(result, where)
+    return result is not None
 
 
 # The current stream's handle by device index, without building a Stream object
@@ -171,10 +201,14 @@ def quantize128(x: torch.Tensor, format: int = E4M3, block: bool = False, direct
     * ``"both"``: ``(codes, scales, codes_t, scales_t)``, from one read of x.
 
     ``pow2``: power-of-two scales. ``out`` may supply the two or four tensors."""
-    ldx = _matrix(x, "x")
     _fp8_format(format)
-    if direction not in ("rows", "cols", "both"):
+    if direction not in _DIRECTIONS:
         raise ValueError("direction must be 'rows', 'cols' or 'both'")
+    if out is None and (_fast or (_fast is None and _bind_fast())):
+        r = _fast.quantize(x, format, bool(block), _DIRECTIONS[direction], bool(pow2))
+        if _made(r, "mx_quantize128"):
+            return r
+    ldx = _matrix(x, "x")
     rows, cols = x.shape
     dev = x.device
     sides = (((rows, cols),) if direction != "cols" else ()) + \
@@ -216,8 +250,12 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
     y)``: h is None without a residual, y None unless ``return_y``. ``h_out``
     may be a buffer for h (``residual`` itself: in place), ``out`` the two
     buffers of codes and scales."""
-    ldx = _matrix(x, "x")
     _fp8_format(format)
+    if out is None and h_out is None and (_fast or (_fast is None and _bind_fast())):
+        r = _fast.norm(x, weight, residual, eps, format, bool(pow2), bool(return_y))
+        if _made(r, "mx_rms_norm_quant128"):
+            return r
+    ldx = _matrix(x, "x")
     rows, cols = x.shape
     dev, dt = x.device, x.dtype
     _contiguous(weight, "weight", dev, dt, (cols,))
@@ -257,6 +295,10 @@ def rms_norm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     ``grad_residual`` (what reaches h from elsewhere) is added to it.
     grad_weight is float32. ``out`` may be a buffer for grad_h (``grad_y`` or
     ``grad_residual`` itself: in place)."""
+    if out is None and (_fast or (_fast is None and _bind_fast())):
+        r = _fast.norm_bwd(grad_y, h, weight, eps, grad_residual)
+        if _made(r, "mx_rms_norm_bwd"):
+            return r
     _matrix(h, "h")
     rows, cols = h.shape
     dev, dt = h.device, h.dtype
@@ -284,11 +326,18 @@ def gemm128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor
     with tile or block scales (by the shape of ``b_scales``). bf16 or float32
     out; ``status``: an optional int32 device tensor set nonzero if one of the
     kernel's waits timed out."""
+    _fp8_format(a_format, "a_format")
+    _fp8_format(b_format, "b_format")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if out is None and status is None and (_fast or (_fast is None and _bind_fast())):
+        r = _fast.gemm(a_codes, a_scales, b_codes, b_scales, a_format, b_format,
+                       out_dtype == torch.float32)
+        if _made(r, "mx_gemm128"):
+            return r
     if not isinstance(a_codes, torch.Tensor) or not a_codes.is_cuda:
         raise ValueError("a_codes must be a CUDA tensor")
     dev = a_codes.device
-    _fp8_format(a_format, "a_format")
-    _fp8_format(b_format, "b_format")
     lda = _codes(a_codes, "a_codes", dev)
     M, K = a_codes.shape
     ldb = _codes(b_codes, "b_codes", dev, cols=K)
@@ -300,8 +349,6 @@ def gemm128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor
     block = b_scales.dim() == 2 and b_scales.shape[0] == (N + 127) // 128 and \
         (N > 1 or b_scales.is_contiguous())
     ldsb = _scales(b_scales, "b_scales", dev, N, K, block)
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be bfloat16 or float32")
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     else:

@@ -449,3 +449,67 @@ def test_norm_gradient_in_a_graph(mx, cuda):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_both_marshalling_paths_give_the_same(mx, cuda):
+    """The C++ module makes the plain calls, Python those with buffers of the
+    caller's: same tensors, layouts included. An unusual call is left to Python."""
+    from fp8_quantization_mx_b200 import ops128
+    x, r = values(130, 300, torch.bfloat16, 1), values(130, 300, torch.bfloat16, 2)
+    w = torch.ones(300, device=cuda, dtype=torch.bfloat16)
+    wq = mx.quantize128(values(200, 300, torch.bfloat16, 3), block=True)
+    calls = [lambda: mx.quantize128(x, E5M2, direction="both", pow2=True),
+             lambda: mx.quantize128(x, block=True, direction="cols"),
+             lambda: mx.rms_norm_quantize(x, w, r, return_y=True), lambda: mx.rms_norm_quantize(x, w),
+             lambda: mx.rms_norm_bwd(x, r, w, grad_residual=x),
+             lambda: mx.gemm128(*mx.quantize128(x), *wq, out_dtype=torch.float32)]
+    assert ops128._fast or ops128._bind_fast()
+    fast, was = [c() for c in calls], ops128._fast
+    try:
+        ops128._fast = False
+        slow = [c() for c in calls]
+    finally:
+        ops128._fast = was
+    for a, b in zip(fast, slow):
+        for s, t in zip(a if isinstance(a, tuple) else (a,), b if isinstance(b, tuple) else (b,)):
+            assert (s is None) == (t is None)
+            if s is not None:
+                assert torch.equal(s, t) and s.stride() == t.stride() and s.dtype == t.dtype
+    assert was.quantize(x.double(), E4M3, False, 1, False) is None
+    assert was.gemm(x, x, x, x, E4M3, E4M3, False) is None
+    assert was.norm(x, w[:299], None, 1e-6, E4M3, False, False) is None
+    assert was.norm(x, w, None, "eps", E4M3, False, False) is None
+    assert was.norm(x, w, None, -1.0, E4M3, False, False) == 1       # the library's refusal
+    with pytest.raises(mx.MXError):
+        mx.rms_norm_quantize(x, w, eps=-1.0)
+
+
+def test_tensor_layer_refuses(mx, cuda):
+    x, w = torch.zeros(8, 256, device=cuda), torch.zeros(256, device=cuda)
+    c, s = mx.quantize128(x)
+    bad = [
+        (lambda: mx.quantize128(x.double()), "bfloat16"), (lambda: mx.quantize128(x[0]), "rows, cols"),
+        (lambda: mx.quantize128(x.t()), "contiguous rows"), (lambda: mx.quantize128(x, 0), "E4M3"),
+        (lambda: mx.quantize128(x, direction="up"), "direction"),
+        (lambda: mx.quantize128(x.expand(8, 256)[:1].expand(8, 256)), "overlapping"),
+        (lambda: mx.quantize128(x, out=(c,)), "2 tensors"),
+        (lambda: mx.quantize128(x, out=(c[:, :128], s)), "must be"),
+        (lambda: mx.quantize128(x, out=(c, s.contiguous())), "tile by tile"),
+        (lambda: mx.quantize128(x, out=(torch.zeros(8, 256, device=cuda), s)), "uint8"),
+        (lambda: mx.quantize128(x[:, :250], out=(torch.empty(8, 250, dtype=torch.uint8, device=cuda), s)),
+         "16 bytes apart"),
+        (lambda: mx.rms_norm_quantize(x, w.bfloat16()), "weight"), (lambda: mx.rms_norm_quantize(x, w[:5]), "weight"),
+        (lambda: mx.rms_norm_quantize(x, w, x[:4]), "residual"), (lambda: mx.rms_norm_quantize(x, w, h_out=x), "h_out"),
+        (lambda: mx.rms_norm_bwd(x, x.t().contiguous().t(), w), "contiguous"),
+        (lambda: mx.rms_norm_bwd(None, x, w), "grad_y"), (lambda: mx.rms_norm_bwd(x, x, w, grad_residual=x[:4]), "grad_residual"),
+        (lambda: mx.gemm128(c, s, c[:, :128], s), "b_codes"), (lambda: mx.gemm128(c, s.contiguous(), c, s), "a_scales"),
+        (lambda: mx.gemm128(c, s, c, s[:4]), "b_scales"), (lambda: mx.gemm128(c, s, c, s, a_format=3), "a_format"),
+        (lambda: mx.gemm128(c, s, c, s, out_dtype=torch.float16), "out_dtype"),
+        (lambda: mx.gemm128(c, s, c, s, out=torch.empty(8, 9, device=cuda)), "out"),
+        (lambda: mx.gemm128(c, s, c, s, status=torch.zeros(1, device=cuda)), "status"),
+        # a view whose last row's padding lies outside the storage
+        (lambda: mx.gemm128(c.view(-1)[:2040].as_strided((8, 250), (256, 1), 6), s, c, s), "outside its storage"),
+    ]
+    for call, words in bad:
+        with pytest.raises(ValueError, match=words):
+            call()
