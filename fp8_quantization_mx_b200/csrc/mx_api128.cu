@@ -160,6 +160,7 @@ int mx_gemm128(const void* a_codes, int64_t lda, const float* a_scales, int64_t 
   u.K = K;
   u.out_fp32 = out_fp32;
   u.d = d;
+  u.ldd = N;
   u.status = status;
   return from_cuda(mxk::launch_gemm128(u, nullptr, cs));
 }

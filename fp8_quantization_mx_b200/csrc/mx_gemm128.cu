@@ -797,7 +797,7 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
 //   Clusters are not free to pack: 17 of 8 CTAs run as two waves (13.5 us, 9.5
 //   with clusters of 4), since a cluster stays within one of the GPU's SM groups.
 Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int clusters4,
-                     int clusters8) {
+                     int clusters8, double* us) {
   struct Cut {
     int bn, swap;
     double kb_block, kb_tile, tail;   // per K-block with block / tile weights, per wave
@@ -823,12 +823,13 @@ Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int
       const double t = static_cast<double>(waves) *
                            (static_cast<double>((nk + split - 1) / split) *
                                 (b_block ? c.kb_block : c.kb_tile) + c.tail) + kJoin[i];
-      if (best.bn == 0 || t < best_t) {
+      if (best_t == 0.0 || t < best_t) {
         best = {c.bn, c.swap, split};
         best_t = t;
       }
     }
   }
+  *us = best_t;
   return best;
 }
 
@@ -869,21 +870,17 @@ cudaError_t device_clusters(int dev, int* c4, int* c8) {
 
 }  // namespace
 
-cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = device_sms(&dev, &sms);
-  int c4 = 0, c8 = 0;
-  if (e == cudaSuccess && !plan) e = device_clusters(dev, &c4, &c8);
-  if (e != cudaSuccess) return e;
-  const Plan128 p = plan ? *plan : plan_gemm128(u.M, u.N, u.K, u.b_block, sms, c4, c8);
+namespace {
+
+cudaError_t launch_one(const Gemm128& u, const Plan128& p, int dev, int sms, cudaStream_t st) {
   Gemm128Args g{};
   g.d = static_cast<uint8_t*>(u.d);
   g.status = u.status;
-  g.ldd = u.N;
+  g.ldd = u.ldd;
   g.nk = static_cast<int>((u.K + 127) / 128);
   g.split = p.bn == 256 ? 1 : p.split;
   g.out_fp32 = u.out_fp32;
-  g.vec = u.N * (u.out_fp32 ? 4 : 2) % 16 == 0;
+  g.vec = u.ldd * (u.out_fp32 ? 4 : 2) % 16 == 0;
   if (p.swap) {
     if (p.bn == 16) return launch<Cfg<16, true, true, false, 10>>(u, g, dev, sms, st);
     if (p.bn == 32) return launch<Cfg<32, true, true, false, 10>>(u, g, dev, sms, st);
@@ -897,6 +894,68 @@ cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t s
   if (p.bn == 64) return launch<Cfg<64, true, false, false, 8>>(u, g, dev, sms, st);
   if (p.bn == 128) return launch<Cfg<128, true, false, false, 6>>(u, g, dev, sms, st);
   return launch<Cfg<256, true, false, true, 6>>(u, g, dev, sms, st);
+}
+
+// Rows m0.. and columns n0.. of D (m0, n0 multiples of 256).
+Gemm128 part_of(const Gemm128& u, int64_t m0, int64_t M, int64_t n0, int64_t N) {
+  Gemm128 v = u;
+  v.a = static_cast<const uint8_t*>(u.a) + m0 * u.lda;
+  v.a_scales = u.a_scales + m0;
+  v.b = static_cast<const uint8_t*>(u.b) + n0 * u.ldb;
+  v.b_scales = u.b_scales + (u.b_block ? n0 / 128 * ((u.K + 127) / 128) : n0);
+  v.d = static_cast<uint8_t*>(u.d) + (m0 * u.ldd + n0) * (u.out_fp32 ? 4 : 2);
+  v.M = M;
+  v.N = N;
+  return v;
+}
+
+}  // namespace
+
+// Sizes a little over a multiple of 256 cost whole tiles, at times a whole wave
+// of them: rows and columns past the multiple are then products of their own,
+// if by the model that is cheaper (4099 x 2056 x 8192: one wave of three, 81 ->
+// 70 us). A further launch on the stream costs 3 us.
+cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st) {
+  constexpr double kLaunch = 3.0;
+  int dev = 0, sms = 0, c4 = 0, c8 = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  if (plan) return launch_one(u, *plan, dev, sms, st);
+  e = device_clusters(dev, &c4, &c8);
+  if (e != cudaSuccess) return e;
+  const auto cost = [&](const Gemm128& v, Plan128* p) {
+    double us = 0.0;
+    *p = plan_gemm128(v.M, v.N, v.K, v.b_block, sms, c4, c8, &us);
+    return us;
+  };
+  Plan128 whole{};
+  double best = cost(u, &whole);
+  Gemm128 parts[3] = {u};
+  Plan128 plans[3] = {whole};
+  int n = 1;
+  const int64_t m0 = u.M / 256 * 256, n0 = u.N / 256 * 256;
+  for (int cut = 1; cut < 4; ++cut) {   // rows, columns, both
+    const int64_t m = cut & 1 ? m0 : u.M, c = cut & 2 ? n0 : u.N;
+    if (m == 0 || c == 0 || ((cut & 1) && m == u.M) || ((cut & 2) && c == u.N)) continue;
+    Gemm128 q[3];
+    Plan128 qp[3];
+    int k = 0;
+    q[k++] = part_of(u, 0, m, 0, c);
+    if (c < u.N) q[k++] = part_of(u, 0, m, c, u.N - c);
+    if (m < u.M) q[k++] = part_of(u, m, u.M - m, 0, u.N);
+    double us = kLaunch * (k - 1);
+    for (int i = 0; i < k; ++i) us += cost(q[i], &qp[i]);
+    if (us < best) {
+      best = us;
+      n = k;
+      for (int i = 0; i < k; ++i) {
+        parts[i] = q[i];
+        plans[i] = qp[i];
+      }
+    }
+  }
+  for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_one(parts[i], plans[i], dev, sms, st);
+  return e;
 }
 
 }  // namespace mxk

@@ -17,7 +17,8 @@ struct Gemm128 {
   int b_e5m2, b_block;
   int64_t M, N, K;
   int out_fp32;
-  void* d;                 // [M, N]
+  void* d;                 // [M, ldd]
+  int64_t ldd;
   int* status;             // nullable
 };
 
@@ -27,9 +28,10 @@ struct Plan128 {
   int bn, swap, split;
 };
 
-// sms, and how many clusters of 4 and of 8 one-per-SM CTAs run at once.
+// sms, and how many clusters of 4 and of 8 one-per-SM CTAs run at once. *us: the
+// model's time, without a launch's own.
 Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int clusters4,
-                     int clusters8);
+                     int clusters8, double* us);
 
 // plan: NULL for plan_gemm128's choice on the current device.
 cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st);

@@ -261,7 +261,8 @@ def operand(rows, K, fmt, block, seed):
 GEMM_SHAPES = [(1, 128, 128), (1, 1, 1), (7, 130, 96), (16, 1536, 2048), (17, 392, 640), (33, 264, 1000),
                (64, 512, 4096), (65, 200, 384), (100, 72, 257), (128, 1024, 2048), (200, 2056, 512),
                (300, 520, 1111), (1, 2048, 4100), (1500, 129, 128), (2200, 2056, 256),
-               (129, 4096, 128), (3, 5, 7000)]
+               (129, 4096, 128), (3, 5, 7000), (2563, 2056, 1500),
+               (4099, 1030, 640), (1024, 4872, 1024)]
 
 
 @pytest.mark.parametrize("block", [True, False])
