@@ -106,6 +106,7 @@ struct Cfg {
   static constexpr uint32_t kStaging = SWAP ? 0 : kWork * 32 * kStgRow;
   static constexpr int kBars = S + kHalves * (S + NBUF) + 1 + 4;
   static constexpr uint32_t kSmem = S * kStage + kStaging + 2 * kSlot + 8 * kBars + 16 + 1024;
+  static_assert((S & (S - 1)) == 0 && (NBUF & (NBUF - 1)) == 0, "counters");
   static_assert(kHalves == 1 || kParts == 2, "a half per part");
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -576,15 +577,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int h = C::kHalves == 2 ? part : 0;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                (C::kHalves == 2 ? h * C::NBUF * C::kUnitN : part * C::kCols);
-    Ring<C::S> st;
-    Ring<C::NBUF> tb;
-    Ring<2> ss;
+    // K-blocks and slots so far: stage, accumulator, slot and their parities are
+    // its low bits (all powers of two)
+    uint32_t n = 0, nslot = 0;
     // where accumulators are given back: to the CTA that issues the MMAs
     const uint32_t free0 = C::PAIR ? tc::mapa(sm.tempty(h, 0), 0) : sm.tempty(h, 0);
     // this thread's row scale and its part's column scales in a slot
-    const float* row_scale =
-        sm.scl_ptr + (C::QCOL ? 0 : part * C::kCols / kRows) * kRows + quarter * 32 + lane;
-    const float* col_scale = sm.scl_ptr + C::kRowSlot / 4 + part * C::kCols;
+    const int row_scale = (C::QCOL ? 0 : part * C::kCols / kRows) * kRows + quarter * 32 + lane;
+    const int col_scale = C::kRowSlot / 4 + part * C::kCols;
+    const uint32_t done0 = sm.done(h, 0);
     bool ok = true;
     for (int64_t t = t_first; ok && t < ntiles; t += t_step) {
       int64_t p, q;
@@ -593,73 +594,78 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       float acc[C::kCols];
 #pragma unroll
       for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int at = (kb - kb0) & (C::kBatch - 1);
-        const bool last = at == C::kBatch - 1 || kb + 1 == kb1;   // of its slot
-        if (at == 0)
-          ok &= tc::mbar_wait(sm.sfull(ss.slot), ss.par, sm.abort_flag, g.status, kStatusSums);
-        const int slot = ss.slot * (C::kSlot / 4);
-        const float s = row_scale[slot + at * C::kRowSets * kRows];
-        // (after a wait that ran out the loop goes on, every later wait returns
-        // at once, and nothing is stored: tcgen05.ld needs the whole warp)
-        ok &= tc::mbar_wait(sm.done(h, st.slot), st.par, sm.abort_flag, g.status, kStatusSums);
-        __syncwarp();
-        tc::tc_fence_after();
-        // Columns per load, two loads in flight. Column scales come a load ahead
-        // too (read where they are used, their latency took 280 ns per K-block).
-        constexpr int kLd = C::QCOL || C::kCols < 32 ? 16 : 32;
-        const uint32_t taddr = lane_base + tb.slot * C::kUnitN;
-        uint32_t r[2][kLd];
-        float4 f[2][C::QCOL ? kLd / 4 : 1];
-        const float4* qv = reinterpret_cast<const float4*>(col_scale + slot + at * C::BN);
-        tc::tmem_ld_start(taddr, r[0]);
-        if constexpr (C::QCOL)
-#pragma unroll
-          for (int i = 0; i < kLd / 4; ++i) f[0][i] = qv[i];
-        tc::tmem_ld_wait(r[0]);
-#pragma unroll
-        for (int c0 = 0; c0 < C::kCols; c0 += kLd) {
-          constexpr int kMask = 1;
-          uint32_t(&now)[kLd] = r[(c0 / kLd) & kMask];
-          uint32_t(&next)[kLd] = r[(c0 / kLd + 1) & kMask];
-          if (c0 + kLd < C::kCols) {
-            tc::tmem_ld_start(taddr + c0 + kLd, next);
-            if constexpr (C::QCOL)
-#pragma unroll
-              for (int i = 0; i < kLd / 4; ++i)
-                f[(c0 / kLd + 1) & kMask][i] = qv[(c0 + kLd) / 4 + i];
-          } else {
-            // the accumulator has been read
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (C::PAIR) tc::mbar_arrive_relaxed_cluster(free0 + 8 * tb.slot);
-              else tc::mbar_arrive_relaxed(free0 + 8 * tb.slot);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kLd; i += 4) {
-            float4 q = make_float4(s, s, s, s);
-            if constexpr (C::QCOL) {
-              const float4 v = f[(c0 / kLd) & kMask][i / 4];
-              const float2 lo = __fmul2_rn(make_float2(v.x, v.y), make_float2(s, s));
-              const float2 hi = __fmul2_rn(make_float2(v.z, v.w), make_float2(s, s));
-              q = make_float4(lo.x, lo.y, hi.x, hi.y);
-            }
-            fma2(acc[c0 + i], acc[c0 + i + 1], q.x, q.y, now[i], now[i + 1]);
-            fma2(acc[c0 + i + 2], acc[c0 + i + 3], q.z, q.w, now[i + 2], now[i + 3]);
-          }
-          if (c0 + kLd < C::kCols) tc::tmem_ld_wait(next);
-        }
-        if (last) {
+      for (int kb = kb0; kb < kb1; kb += C::kBatch, ++nslot) {
+        ok &= tc::mbar_wait(sm.sfull(nslot & 1), (nslot >> 1) & 1, sm.abort_flag, g.status, kStatusSums);
+        const float* slot = sm.scl_ptr + (nslot & 1) * (C::kSlot / 4);
+        // (not unrolled: the loop's length in instructions is what the issuing
+        // warps, which share the schedulers, have to be fetched past; unrolled
+        // by four, 8192^3 took 595 us, 432 as it is)
+#pragma unroll 1
+        for (int at = 0; at < C::kBatch; ++at) {
+          if (kb + at >= kb1) break;
+          const float s = slot[row_scale + at * C::kRowSets * kRows];
+          // (after a wait that ran out the loop goes on, every later wait returns
+          // at once, and nothing is stored: tcgen05.ld needs the whole warp)
+          ok &= tc::mbar_wait(done0 + 8 * (n & (C::S - 1)), (n / C::S) & 1, sm.abort_flag, g.status,
+                              kStatusSums);
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(sm.sempty(ss.slot));
-          ss.next();
+          tc::tc_fence_after();
+          const uint32_t b = n & (C::NBUF - 1);
+          ++n;
+          // Columns per load, two loads in flight. Column scales come a load ahead
+          // too (read where they are used, their latency took 280 ns per K-block).
+          constexpr int kLd = C::QCOL || !C::PAIR ? 16 : 32;
+          const uint32_t taddr = lane_base + b * C::kUnitN;
+          uint32_t r[2][kLd];
+          float4 f[2][C::QCOL ? kLd / 4 : 1];
+          const float4* qv = reinterpret_cast<const float4*>(slot + col_scale + at * C::BN);
+          tc::tmem_ld_start(taddr, r[0]);
+          if constexpr (C::QCOL)
+#pragma unroll
+            for (int i = 0; i < kLd / 4; ++i) f[0][i] = qv[i];
+          tc::tmem_ld_wait(r[0]);
+#pragma unroll
+          for (int c0 = 0; c0 < C::kCols; c0 += kLd) {
+            constexpr int kMask = 1;
+            uint32_t(&now)[kLd] = r[(c0 / kLd) & kMask];
+            uint32_t(&next)[kLd] = r[(c0 / kLd + 1) & kMask];
+            if (c0 + kLd < C::kCols) {
+              tc::tmem_ld_start(taddr + c0 + kLd, next);
+              if constexpr (C::QCOL)
+#pragma unroll
+                for (int i = 0; i < kLd / 4; ++i)
+                  f[(c0 / kLd + 1) & kMask][i] = qv[(c0 + kLd) / 4 + i];
+            } else {
+              // the accumulator has been read
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (C::PAIR) tc::mbar_arrive_relaxed_cluster(free0 + 8 * b);
+                else tc::mbar_arrive_relaxed(free0 + 8 * b);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kLd; i += 4) {
+              float4 q = make_float4(s, s, s, s);
+              if constexpr (C::QCOL) {
+                const float4 v = f[(c0 / kLd) & kMask][i / 4];
+                const float2 lo = __fmul2_rn(make_float2(v.x, v.y), make_float2(s, s));
+                const float2 hi = __fmul2_rn(make_float2(v.z, v.w), make_float2(s, s));
+                q = make_float4(lo.x, lo.y, hi.x, hi.y);
+              }
+              fma2(acc[c0 + i], acc[c0 + i + 1], q.x, q.y, now[i], now[i + 1]);
+              fma2(acc[c0 + i + 2], acc[c0 + i + 3], q.z, q.w, now[i + 2], now[i + 3]);
+            }
+            if (c0 + kLd < C::kCols) tc::tmem_ld_wait(next);
+          }
         }
-        st.next();
-        tb.next();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sm.sempty(nslot & 1));
       }
-      if (!__all_sync(~0u, ok)) break;
+      if (!__all_sync(~0u, ok)) {
+        ok = false;
+        break;
+      }
       if (!C::PAIR && g.split > 1) {
         // the ring is idle: every K-block loaded has been multiplied. (The
         // generic writes below follow the MMAs' reads through tfull.)
@@ -788,14 +794,16 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
 }  // namespace
 
 // The cheapest cut by a model of the time: waves of clusters times the K-blocks
-// of a CTA times a K-block's time, plus what joining a split costs. Measured on
-// a B200 (us; a K-block of each tile in a full wave, one join per size):
+// of a CTA times a K-block's time, plus what joining a split costs (more for
+// wide tiles, whose partial sums cross the cluster). Its figures are measured
+// (us), and it chose within 6% of the best cut at all but a few of 80 sizes:
 //   a tile that is finer than needed loses to its number of waves, one that is
-//   coarser leaves SMs idle: 128 x 8192 x 4096 takes 12.6 us in 64-wide tiles,
-//   13.9 in 128-wide ones on twice the CTAs per tile, 19.2 in pairs' tiles;
-//   512 x 8192 x 8192 takes 66 us in 64-wide tiles, 50 and 34.
-//   Clusters are not free to pack: 17 of 8 CTAs run as two waves (13.5 us, 9.5
-//   with clusters of 4), since a cluster stays within one of the GPU's SM groups.
+//   coarser leaves SMs idle: 128 x 8192 x 4096 takes 10.6 us in 64-wide tiles,
+//   13.1 in 128-wide ones on two CTAs each, 18 in pairs' tiles; 512 x 8192 x
+//   8192 takes 66 us in 64-wide tiles, 50 in 128-wide ones, 34 in pairs'.
+//   Clusters are not free to pack: 17 of 8 CTAs run as two waves (12.0 us, 7.6
+//   with clusters of 4), since a cluster stays within one of the GPU's groups of
+//   SMs, and the occupancy query counts one more than ever ran at once.
 Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int clusters4,
                      int clusters8, double* us) {
   struct Cut {
@@ -804,7 +812,7 @@ Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int
   };
   static constexpr Cut kCuts[] = {
       {16, 1, 0.22, 0.22, 0.3}, {32, 1, 0.225, 0.225, 0.4}, {64, 1, 0.25, 0.25, 0.6},
-      {64, 0, 0.19, 0.25, 0.3}, {128, 0, 0.32, 0.55, 1.0},  {256, 0, 0.42, 0.80, 1.5}};
+      {64, 0, 0.19, 0.25, 0.3}, {128, 0, 0.27, 0.36, 1.0},  {256, 0, 0.41, 0.62, 1.5}};
   static constexpr double kJoin[] = {0.0, 0.5, 1.0, 1.3};
   const int64_t nk = (K + 127) / 128;
   Plan128 best{};
@@ -822,7 +830,8 @@ Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int
       const int64_t waves = (tiles + slots - 1) / slots;
       const double t = static_cast<double>(waves) *
                            (static_cast<double>((nk + split - 1) / split) *
-                                (b_block ? c.kb_block : c.kb_tile) + c.tail) + kJoin[i];
+                                (b_block ? c.kb_block : c.kb_tile) + c.tail) +
+                       (i ? kJoin[i] + 0.015 * c.bn : 0.0);
       if (best_t == 0.0 || t < best_t) {
         best = {c.bn, c.swap, split};
         best_t = t;
@@ -840,7 +849,7 @@ cudaError_t device_clusters(int dev, int* c4, int* c8) {
   static std::atomic<int> known[kMaxDevices];   // c4 | c8 << 16, 0 unknown
   int v = known[dev].load(std::memory_order_relaxed);
   if (v == 0) {
-    using C = Cfg<128, false, false, false, 6>;
+    using C = Cfg<128, false, false, false, 4>;
     auto kern = gemm128_kernel<C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(C::kSmem));
@@ -860,7 +869,8 @@ cudaError_t device_clusters(int dev, int* c4, int* c8) {
       e = cudaOccupancyMaxActiveClusters(&n[i], kern, &cfg);
     }
     if (e != cudaSuccess) return e;
-    v = n[0] | n[1] << 16;
+    // (8 groups of SMs hold two clusters of 8 each)
+    v = n[0] | (n[1] < 16 ? n[1] : 16) << 16;
     known[dev].store(v, std::memory_order_relaxed);
   }
   *c4 = v & 0xffff;
@@ -882,18 +892,18 @@ cudaError_t launch_one(const Gemm128& u, const Plan128& p, int dev, int sms, cud
   g.out_fp32 = u.out_fp32;
   g.vec = u.ldd * (u.out_fp32 ? 4 : 2) % 16 == 0;
   if (p.swap) {
-    if (p.bn == 16) return launch<Cfg<16, true, true, false, 10>>(u, g, dev, sms, st);
-    if (p.bn == 32) return launch<Cfg<32, true, true, false, 10>>(u, g, dev, sms, st);
+    if (p.bn == 16) return launch<Cfg<16, true, true, false, 8>>(u, g, dev, sms, st);
+    if (p.bn == 32) return launch<Cfg<32, true, true, false, 8>>(u, g, dev, sms, st);
     return launch<Cfg<64, true, true, false, 8>>(u, g, dev, sms, st);
   }
   if (u.b_block) {
     if (p.bn == 64) return launch<Cfg<64, false, false, false, 8>>(u, g, dev, sms, st);
-    if (p.bn == 128) return launch<Cfg<128, false, false, false, 6>>(u, g, dev, sms, st);
-    return launch<Cfg<256, false, false, true, 6>>(u, g, dev, sms, st);
+    if (p.bn == 128) return launch<Cfg<128, false, false, false, 4>>(u, g, dev, sms, st);
+    return launch<Cfg<256, false, false, true, 4>>(u, g, dev, sms, st);
   }
   if (p.bn == 64) return launch<Cfg<64, true, false, false, 8>>(u, g, dev, sms, st);
-  if (p.bn == 128) return launch<Cfg<128, true, false, false, 6>>(u, g, dev, sms, st);
-  return launch<Cfg<256, true, false, true, 6>>(u, g, dev, sms, st);
+  if (p.bn == 128) return launch<Cfg<128, true, false, false, 4>>(u, g, dev, sms, st);
+  return launch<Cfg<256, true, false, true, 4>>(u, g, dev, sms, st);
 }
 
 // Rows m0.. and columns n0.. of D (m0, n0 multiples of 256).

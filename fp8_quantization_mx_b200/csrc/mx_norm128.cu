@@ -67,15 +67,16 @@ __device__ __forceinline__ float row_rstd(float sum, int64_t cols, float eps) {
   return __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(cols)) + eps);
 }
 
+// Codes of -ny.
 template <bool E5M2>
-__device__ __forceinline__ uint2 encode8(const float (&y)[8], const Divisor& d) {
-  const float2 s = make_float2(d.s, d.s), inv = make_float2(d.inv, d.inv);
+__device__ __forceinline__ uint2 encode8(const float (&ny)[8], const Divisor& d) {
+  const float2 s = make_float2(d.s, d.s), ninv = make_float2(d.ninv, d.ninv);
   float2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 x = make_float2(y[2 * i], y[2 * i + 1]);
+    float2 x = make_float2(ny[2 * i], ny[2 * i + 1]);
     if (d.slow) x = __fmul2_rn(x, make_float2(kLift, kLift));
-    q[i] = div2(x, s, inv);
+    q[i] = div2(x, s, ninv);
   }
   return make_uint2(enc4<E5M2>(q[0].x, q[0].y, q[1].x, q[1].y),
                     enc4<E5M2>(q[2].x, q[2].y, q[3].x, q[3].y));
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
       }
     }
     rt.sum(ss, red, par);
-    const float r = row_rstd(ss[0], a.cols, a.eps);
+    const float r = -row_rstd(ss[0], a.cols, a.eps);   // y negated, as encode8 takes it
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = rt.tid + j * rt.nt;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
         if (a.y) {
           Vec<DT, 8> o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o.set2(e, y[2 * e], y[2 * e + 1]);
+          for (int e = 0; e < 4; ++e) o.set2(e, -y[2 * e], -y[2 * e + 1]);
           o.store(static_cast<T*>(a.y) + row * a.cols + 8 * i);
         }
       }
@@ -254,8 +255,8 @@ __global__ void __launch_bounds__(256) norm128_any_kernel(const NormArgs a) {
     for (int j = 0; j < NJ; ++j) {
       const int64_t c = c0 + tid + 256 * j;
       const Divisor d = sh_div[2 * j + (warp >> 2)];
-      const float v = d.slow ? y[j] * kLift : y[j];
-      const float2 q = div2(make_float2(v, 0.0f), make_float2(d.s, d.s), make_float2(d.inv, d.inv));
+      const float v = d.slow ? -y[j] * kLift : -y[j];
+      const float2 q = div2(make_float2(v, 0.0f), make_float2(d.s, d.s), make_float2(d.ninv, d.ninv));
       if (c < pitch) a.codes[row * a.ldc + c] = static_cast<uint8_t>(enc2<E5M2>(q.x, 0.0f));
       if (c < a.cols) {
         if (a.h) static_cast<T*>(a.h)[row * a.cols + c] = E::from_float(h[j]);

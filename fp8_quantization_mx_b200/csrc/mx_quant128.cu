@@ -53,48 +53,64 @@ constexpr int kThreads = 256;
 // eight lanes that write a column of their own group hit eight bank quads.
 __device__ __forceinline__ int word_at(int c, int g) { return c * 32 + (g ^ (((c >> 4) & 7) << 2)); }
 
+// Where a column's scale sits in the shared arrays: two floats of padding after
+// 16 columns, so that the eight groups' pairs are in different banks.
+constexpr int kPadded = 128 + 16;
+__device__ __forceinline__ int col_at(int c) { return c + (c >> 4) * 2; }
+
 template <bool E5M2, bool SLOW, int DT>
 __device__ __forceinline__ uint4 encode_row(const Vec<DT, 16>& v, const Divisor& d) {
   uint32_t o[4];
-  const float2 s = make_float2(d.s, d.s), inv = make_float2(d.inv, d.inv);
+  const float2 s = make_float2(d.s, d.s), ninv = make_float2(d.ninv, d.ninv);
   const float2 lift = make_float2(kLift, kLift);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = div2(SLOW ? __fmul2_rn(v.get2(2 * i), lift) : v.get2(2 * i), s, inv);
-    const float2 b = div2(SLOW ? __fmul2_rn(v.get2(2 * i + 1), lift) : v.get2(2 * i + 1), s, inv);
+    const float2 a = div2(SLOW ? __fmul2_rn(v.neg2(2 * i), lift) : v.neg2(2 * i), s, ninv);
+    const float2 b = div2(SLOW ? __fmul2_rn(v.neg2(2 * i + 1), lift) : v.neg2(2 * i + 1), s, ninv);
     o[i] = enc4<E5M2>(a.x, a.y, b.x, b.y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// col_s, col_inv: of the piece's columns, lifted where the scale is tiny (SLOW
+// col_s, col_ninv: of the piece's columns, lifted where the scale is tiny (SLOW
 // takes notice).
 template <bool E5M2, bool SLOW, int DT>
 __device__ __forceinline__ void encode_cols(const Vec<DT, 16> (&v)[4], const float* col_s,
-                                            const float* col_inv, const float* col_lift, int g,
+                                            const float* col_ninv, const float* col_lift, int g,
                                             int sub, uint32_t* out) {
 #pragma unroll
   for (int c2 = 0; c2 < 8; ++c2) {
-    const float2 s = reinterpret_cast<const float2*>(col_s)[sub * 8 + c2];
-    const float2 inv = reinterpret_cast<const float2*>(col_inv)[sub * 8 + c2];
+    const int at = col_at(sub * 16 + 2 * c2);
+    const float2 s = *reinterpret_cast<const float2*>(col_s + at);
+    const float2 ninv = *reinterpret_cast<const float2*>(col_ninv + at);
     float2 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 x = v[i].get2(c2);
-      if constexpr (SLOW) x = __fmul2_rn(x, reinterpret_cast<const float2*>(col_lift)[sub * 8 + c2]);
-      q[i] = div2(x, s, inv);
+      float2 x = v[i].neg2(c2);
+      if constexpr (SLOW) x = __fmul2_rn(x, *reinterpret_cast<const float2*>(col_lift + at));
+      q[i] = div2(x, s, ninv);
     }
     out[word_at(sub * 16 + 2 * c2, g)] = enc4<E5M2>(q[0].x, q[1].x, q[2].x, q[3].x);
     out[word_at(sub * 16 + 2 * c2 + 1, g)] = enc4<E5M2>(q[0].y, q[1].y, q[2].y, q[3].y);
   }
 }
 
+// CTAs per SM that the registers are cut for. What hides a piece's load, sums
+// and stores is other CTAs: 32768 x 4096 both ways took 148, 123, 110, 110 us
+// with 2 to 5 of them, rows alone 74, 74, 66, 63; floats spill beyond 3. (One
+// CTA that loads the next piece ahead, at 2 per SM: 152 and 92 us.)
+template <int DT>
+constexpr int ctas_per_sm(bool rows, bool cols, bool block) {
+  return DT == kFP32 ? 3 : rows && !cols && !block ? 5 : 4;
+}
+
 template <int DT, bool E5M2, bool ROWS, bool COLS, bool BLOCK>
-__global__ void __launch_bounds__(kThreads, 3) quant128_kernel(const Quant128Args a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>(ROWS, COLS, BLOCK)) quant128_kernel(const Quant128Args a) {
   using T = typename Elem<DT>::T;
   __shared__ __align__(16) uint32_t sh_codes[COLS ? 128 * 32 : 4];
-  __shared__ __align__(16) float sh_red[8][BLOCK ? 4 : 128];
-  __shared__ __align__(16) float sh_s[COLS ? 128 : 4], sh_inv[COLS ? 128 : 4], sh_lift[COLS ? 128 : 4];
+  __shared__ __align__(16) float sh_red[8][BLOCK || !COLS ? 4 : 128];
+  constexpr int kCols = COLS && !BLOCK ? kPadded : 2;
+  __shared__ __align__(16) float sh_s[kCols], sh_ninv[kCols], sh_lift[kCols];
   __shared__ int sh_slow;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -228,18 +244,18 @@ __global__ void __launch_bounds__(kThreads, 3) quant128_kernel(const Quant128Arg
         for (int w = 1; w < 8; ++w) mm = amax2(mm, sh_red[w][tid]);
         const float s = tile_scale<E5M2>(mm, a.pow2);
         const Divisor d = divisor(s, mm == 0.0f);
-        sh_s[tid] = d.s;
-        sh_inv[tid] = d.inv;
-        sh_lift[tid] = d.slow ? kLift : 1.0f;
+        sh_s[col_at(tid)] = d.s;
+        sh_ninv[col_at(tid)] = d.ninv;
+        sh_lift[col_at(tid)] = d.slow ? kLift : 1.0f;
         if (d.slow) sh_slow = 1;
         // (columns past the edge: zero tiles; ldst >= cols rounded up to 4)
         if (cb * 128 + tid < ((a.cols + 3) & ~int64_t(3))) a.scales_t[rb * a.ldst + cb * 128 + tid] = s;
       }
       __syncthreads();
       if (sh_slow)
-        encode_cols<E5M2, true, DT>(v, sh_s, sh_inv, sh_lift, g, sub, sh_codes);
+        encode_cols<E5M2, true, DT>(v, sh_s, sh_ninv, sh_lift, g, sub, sh_codes);
       else
-        encode_cols<E5M2, false, DT>(v, sh_s, sh_inv, sh_lift, g, sub, sh_codes);
+        encode_cols<E5M2, false, DT>(v, sh_s, sh_ninv, sh_lift, g, sub, sh_codes);
     }
     __syncthreads();
     // eight lanes write a column's 128 codes; 32 columns at a time

@@ -64,29 +64,31 @@ __device__ __forceinline__ float tile_scale(float amax, bool pow2) {
 
 __device__ __forceinline__ float recip(float s) { return __frcp_rn(s); }
 
-// {x.x / s.x, x.y / s.y} correctly rounded, given inv = 1 / s correctly rounded:
-// a quotient within one unit in the last place, corrected by its exact
-// remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990; the signs keep -0 / s = -0). Ties of the codes
-// are decided on the rounded quotient. Packed: 1.5 instructions per element
-// where a division takes about ten.
-__device__ __forceinline__ float2 div2(float2 x, float2 s, float2 inv) {
-  const float2 q = __fmul2_rn(x, inv);
-  const float2 r = __ffma2_rn(q, s, make_float2(-x.x, -x.y));
-  return __ffma2_rn(make_float2(-r.x, -r.y), inv, q);
+// {x.x / s.x, x.y / s.y} correctly rounded, given nx = -x and ninv = -(1 / s)
+// correctly rounded: a quotient within one unit in the last place, corrected by
+// its exact remainder (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990). Ties of the codes are decided on the
+// rounded quotient. Packed: 1.5 instructions per element where a division takes
+// about ten. The negations are the caller's because packed operands have none
+// (left to the compiler they took as long as the rest); with these signs
+// -0 / s stays -0.
+__device__ __forceinline__ float2 div2(float2 nx, float2 s, float2 ninv) {
+  const float2 q = __fmul2_rn(nx, ninv);
+  const float2 r = __ffma2_rn(q, s, nx);
+  return __ffma2_rn(r, ninv, q);
 }
 
 // A tile's scale with what division by it needs.
 struct Divisor {
-  float s, inv;   // as div2 takes them (both lifted for a tiny scale)
-  bool slow;      // x is to be lifted too
+  float s, ninv;   // as div2 takes them (both lifted for a tiny scale)
+  bool slow;       // x is to be lifted too
 };
 
 __device__ __forceinline__ Divisor divisor(float s, bool zero) {
-  Divisor d{s, recip(s), s < kSlowScale && !zero};
+  Divisor d{s, -recip(s), s < kSlowScale && !zero};
   if (d.slow) {
     d.s *= kLift;
-    d.inv *= 1.0f / kLift;
+    d.ninv *= 1.0f / kLift;
   }
   return d;
 }
@@ -179,7 +181,16 @@ struct Vec {
       return __uint_as_float(w[i]);
     }
   }
-  __device__ __forceinline__ float2 get2(int i) const { return make_float2(get(2 * i), get(2 * i + 1)); }
+  // Elements 2i and 2i + 1, negated.
+  __device__ __forceinline__ float2 neg2(int i) const {
+    if constexpr (DT == kFP32) {
+      return make_float2(__uint_as_float(w[2 * i] ^ 0x80000000u), __uint_as_float(w[2 * i + 1] ^ 0x80000000u));
+    } else {
+      Vec<DT, 8> t;
+      t.w[0] = w[i] ^ 0x80008000u;
+      return make_float2(t.get(0), t.get(1));
+    }
+  }
   // The largest magnitude, NaN kept.
   __device__ __forceinline__ float amax() const {
     if constexpr (DT == kFP32) {
