@@ -110,8 +110,12 @@ struct RowThreads {
 
 // NV vectors of 8 elements per thread: the vectors of a tile are 16
 // neighbouring lanes' (four shuffles give its largest magnitude).
-template <int DT, bool E5M2, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
+// HALF: at most 256 threads with two vectors each, registers for three CTAs of
+// 256 (floats two): 16387 x 4096 took 84.7 us with two of them, 78.2 with
+// three, 92 with four.
+template <int DT, bool E5M2, int NV, bool WARP, bool HALF = false>
+__global__ void __launch_bounds__(WARP || NV == 1 || HALF ? 256 : 512,
+                                  NV == 1 ? 4 : HALF ? (DT == kFP32 ? 2 : 3) : 1)
     norm128_kernel(const NormArgs a) {
   using T = typename Elem<DT>::T;
   __shared__ float red[2][32];
@@ -501,18 +505,19 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, i
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // How a row of nvec vectors is spread: up to 1024 elements one warp (one, two
-// or four vectors a lane), up to 2048 a CTA with one vector a thread, up to
-// 8192 two and up to 16384 four (512 threads at most); beyond, the kernel for
-// any size.
+// or four vectors a lane), up to 8192 a CTA with two vectors a thread, up to
+// 16384 four (512 threads at most); beyond, the kernel for any size. A few rows
+// of up to 2048 elements take one vector a thread: what counts is one row's
+// time (1 x 2048: 1.8 us, 2.06 with two; 16387 x 2048: 44.3 us, 40.5 with two).
 constexpr int64_t kMaxVecCols = 16384;
 struct Shape {
   bool warp;
   int nv;
   unsigned nt;
 };
-Shape shape_of(int64_t nvec) {
+Shape shape_of(int64_t nvec, int64_t rows, int sms) {
   if (nvec <= 128) return {true, nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 256};
-  const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  const int nv = nvec <= 256 && rows <= 4 * sms ? 1 : nvec <= 1024 ? 2 : 4;
   return {false, nv, static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)};
 }
 
@@ -534,20 +539,24 @@ cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
                                        : norm128_any_kernel<DT, E5M2, 16>;
     return launch_dependent(kern, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, st, 1, a);
   }
-  const Shape s = shape_of((a.cols + 15) / 16 * 2);   // with the codes' padding
+  const Shape s = shape_of((a.cols + 15) / 16 * 2, a.rows, sms);   // with the codes' padding
+  const bool half = !s.warp && s.nv == 2 && s.nt <= 256;
   const auto kern = s.warp ? (s.nv == 1   ? norm128_kernel<DT, E5M2, 1, true>
                               : s.nv == 2 ? norm128_kernel<DT, E5M2, 2, true>
                                           : norm128_kernel<DT, E5M2, 4, true>)
                            : (s.nv == 1   ? norm128_kernel<DT, E5M2, 1, false>
+                              : half      ? norm128_kernel<DT, E5M2, 2, false, true>
                               : s.nv == 2 ? norm128_kernel<DT, E5M2, 2, false>
                                           : norm128_kernel<DT, E5M2, 4, false>);
-  const int64_t grid = grid_for(s, a.rows, sms, s.nv == 1 ? 1024 : s.nv == 2 ? 704 : 512);
+  const int64_t grid = grid_for(s, a.rows, sms, s.nv == 1   ? 1024
+                                                : half      ? (DT == kFP32 ? 512 : 768)
+                                                : s.nv == 2 ? 704 : 512);
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), 0, st, 1, a);
 }
 
 template <int DT>
 cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaStream_t st) {
-  const Shape s = shape_of(a.cols / 8);
+  const Shape s = shape_of(a.cols / 8, a.rows, sms);
   // (the kernels for any size: 256 threads, four CTAs per SM up to 2048 columns)
   const int64_t any = (a.cols <= 2048 ? 4 : 2) * sms;
   int64_t grid = vec ? grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512)
