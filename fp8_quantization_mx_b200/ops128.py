@@ -439,10 +439,19 @@ class FP8NormLinear128(torch.autograd.Function):
         return gx, gx if ctx.has_residual else None, gn, gw, None, None
 
 
+def _layer_inputs(**tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+
+
 def linear128(x: torch.Tensor, weight: torch.Tensor, grad_format: int = E4M3) -> torch.Tensor:
     """x weight^T with FP8 operands in all three products of training (see
     ``FP8Linear128``). x bfloat16 [..., K], weight bfloat16 [N, K];
     ``grad_format``: the output gradient's FP8 format."""
+    _layer_inputs(x=x, weight=weight)
     y = FP8Linear128.apply(x.reshape(-1, x.shape[-1]), weight, grad_format)
     return y.view(*x.shape[:-1], weight.shape[0])
 
@@ -452,7 +461,11 @@ def rms_norm_linear128(x: torch.Tensor, norm_weight: torch.Tensor, weight: torch
     """``(y weight^T, h)``: h = x + residual (x itself without one), y =
     RMSNorm(h), the product in FP8 from the norm's own codes. Shapes as
     ``linear128``."""
+    _layer_inputs(x=x, norm_weight=norm_weight, weight=weight,
+                  **({} if residual is None else {"residual": residual}))
     shape = x.shape
+    if residual is not None and residual.shape != shape:
+        raise ValueError(f"residual must be {list(shape)}, got {list(residual.shape)}")
     res = None if residual is None else residual.reshape(-1, shape[-1]).contiguous()
     out, h = FP8NormLinear128.apply(x.reshape(-1, shape[-1]), res, norm_weight, weight, eps,
                                     grad_format)

@@ -514,3 +514,87 @@ def test_tensor_layer_refuses(mx, cuda):
     for call, words in bad:
         with pytest.raises(ValueError, match=words):
             call()
+
+
+def test_layers_without_tokens_and_of_one_dimension(mx, cuda):
+    _, _, nw, w = layer_inputs(1, 256, 136)
+    w.requires_grad_()
+    x = torch.empty(0, 256, device=cuda, dtype=torch.bfloat16, requires_grad=True)
+    y, h = mx.rms_norm_linear128(x, nw, w)
+    (mx.linear128(x, w).sum() + y.sum()).backward()
+    assert y.shape == (0, 136) and x.grad.shape == (0, 256) and not w.grad.any()
+    one = layer_inputs(1, 256, 136)[0]
+    assert torch.equal(mx.linear128(one[0], w), mx.linear128(one, w)[0])
+
+
+def test_layers_refuse(mx, cuda):
+    x, r, nw, w = layer_inputs(4, 256, 136)
+    for call in (lambda: mx.linear128(x.float(), w), lambda: mx.linear128(x, w.float()),
+                 lambda: mx.linear128(x, w[:, :128]), lambda: mx.rms_norm_linear128(x, nw.float(), w),
+                 lambda: mx.rms_norm_linear128(x, nw, w, residual=r[:2]),
+                 lambda: mx.rms_norm_linear128(x, nw, w, residual=r.float())):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_norm_in_place_of_x(mx, cuda):
+    for cols in (512, 509, 8200):
+        x, r = values(9, cols, torch.float16, 1), values(9, cols, torch.float16, 2)
+        x = x.contiguous()
+        w = torch.ones(cols, device=cuda, dtype=torch.float16)
+        want = mx.rms_norm_quantize(x, w, r)
+        got = mx.rms_norm_quantize(x, w, r, h_out=x)
+        for a, b in zip(got[:3], want[:3]):
+            assert torch.equal(a, b)
+
+
+def test_calls_on_two_streams_at_once(mx, cuda):
+    """Nothing is shared between calls: two streams at once give what each gives
+    alone, many times over."""
+    x, r, nw, w = layer_inputs(300, 1024, 1536)
+    wq = mx.quantize128(w, block=True)
+
+    def work(a, b):
+        c, s, h, _ = mx.rms_norm_quantize(a, nw, b)
+        return mx.gemm128(c, s, *wq), *mx.rms_norm_bwd(a, h, nw), *mx.quantize128(a, direction="both")
+
+    want = [work(x, r), work(r, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, (a, b) in enumerate(((x, r), (r, x))):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(work(a, b))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_offsets_beyond_32_bits(mx, cuda):
+    """2.3e9 elements: the last rows come out as they do alone."""
+    rows, cols, tail = 70016, 32768, 128
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=cuda)
+    g = torch.Generator(device=cuda).manual_seed(0)
+    for i in range(0, rows, 4376):
+        x[i:i + 4376] = torch.randn(4376, cols, generator=g, device=cuda)
+    w = torch.ones(cols, device=cuda, dtype=torch.bfloat16)
+    last = x[-tail:].clone()
+    c, s, ct, st = mx.quantize128(x, direction="both")
+    lc, ls, lct, lst = mx.quantize128(last, direction="both")
+    assert torch.equal(c[-tail:], lc) and torch.equal(s[-tail:], ls)
+    assert torch.equal(ct[:, -tail:], lct) and torch.equal(st[:, -1:], lst)
+    b = mx.quantize128(last[:40], block=True)
+    d = mx.gemm128(c, s, *b, out_dtype=torch.float32)
+    v = [P.decode(q.cpu().numpy(), E4M3) * P.spread(z.cpu().numpy(), q.shape[0], cols, k)
+         for q, z, k in ((lc, ls, False), (*b, True))]
+    mag = np.abs(v[0]) @ np.abs(v[1]).T
+    assert np.all(np.abs(f64(d[-tail:]) - v[0] @ v[1].T) <= (256 + cols / 128 + 12) * U32 * mag)
+    del ct, st, d
+    nc, ns, h, _ = mx.rms_norm_quantize(x, w, x)
+    mc, ms, mh, _ = mx.rms_norm_quantize(last, w, last)
+    assert torch.equal(nc[-tail:], mc) and torch.equal(ns[-tail:], ms) and torch.equal(h[-tail:], mh)
+    del nc, ns, c, s
+    gh, _ = mx.rms_norm_bwd(x, h, w)
+    assert torch.equal(gh[-tail:], mx.rms_norm_bwd(last, mh, w)[0])
