@@ -262,7 +262,12 @@ GEMM_SHAPES = [(1, 128, 128), (1, 1, 1), (7, 130, 96), (16, 1536, 2048), (17, 39
                (64, 512, 4096), (65, 200, 384), (100, 72, 257), (128, 1024, 2048), (200, 2056, 512),
                (300, 520, 1111), (1, 2048, 4100), (1500, 129, 128), (2200, 2056, 256),
                (129, 4096, 128), (3, 5, 7000), (2563, 2056, 1500),
-               (4099, 1030, 640), (1024, 4872, 1024)]
+               (4099, 1030, 640), (1024, 4872, 1024),
+               # every tile width and orientation, with K split 1, 2, 4 and 8 ways
+               (1, 32, 1289), (2, 33, 1168), (129, 4968, 84), (135, 160, 2563), (257, 149, 3686),
+               (265, 336, 4927), (284, 135, 2597), (292, 399, 1697), (340, 386, 1466), (397, 264, 1831),
+               (548, 949, 3685), (685, 343, 3379), (775, 283, 2005), (900, 3656, 78), (1265, 536, 5790),
+               (1329, 1916, 5019), (1860, 1245, 424), (2838, 1865, 4884)]
 
 
 @pytest.mark.parametrize("block", [True, False])
