@@ -7,20 +7,38 @@
 // every K-block of 128 is accumulated by itself in tensor memory and added,
 // scaled, to float sums in registers:
 //   warp 0     TMA: one K-block of both operands per stage (128 bytes per row:
-//              one 128-byte swizzle atom), S stages; the column scales' ring
-//   warp 1     one thread issues the four tcgen05.mma.kind::f8f6f4 (K = 32)
-//              of a K-block into the next of NBUF accumulators
+//              one 128-byte swizzle atom), S stages
+//   warps 1-2  one thread each issues the four tcgen05.mma.kind::f8f6f4 (K = 32)
+//              of its half of the columns, or of every other K-block, into the
+//              next of NBUF accumulators
+//   warp 3     the scales of four K-blocks at a time into shared memory
 //   warps 4..  accumulator -> registers (tcgen05.ld, one row per thread),
 //              acc += (s_row s_col) t with packed multiply-adds, accumulator
 //              released; after the last K-block the tile is stored
 // so the vector work of one K-block runs beside the MMAs of the next.
 //
-// A tile is 128 rows of one operand ("rows": MMA A) by BN of the other
-// ("columns": MMA B). Few tokens: the weights take the row side (128 of N per
-// tile) and the tokens the column side, BN = 16, 32 or 64, so that no MMA row
-// is wasted and the weights are read once (SWAP). Too few tiles to fill the
-// SMs: a cluster of 2, 4 or 8 CTAs splits K, and each CTA adds up its share of
-// the tile over the cluster's shared memory, in rank order (no atomics).
+// Tiles, rows (MMA A) x columns (MMA B):
+//   256 x 256  a pair of CTAs (cta_group::2), each with 128 of the rows and half
+//              of the columns in its shared memory: large products
+//   128 x 128, 128 x 64   one CTA
+//   128 x 64, 32, 16 with the weights on the row side and the tokens on the
+//              column side (SWAP): few tokens, no MMA row wasted, the weights
+//              read once
+// Where tiles are too few to fill the SMs a cluster of 2, 4 or 8 CTAs splits K,
+// and each CTA adds up its share of the tile over the cluster's shared memory,
+// in rank order (no atomics).
+//
+// What bounds it. One K-block of a pair's tile is 512 clocks of MMA; with
+// nothing but the loads and MMAs it took 344 ns at the clock that the power
+// limit left (3.6 PFLOP/s), as a whole 382 ns with block scales and 570 with
+// column scales, whose second multiplication fills the FMA pipe for as long as
+// the MMAs run. 8192^3 takes 431 us (2.55 PFLOP/s) in bursts and 516 us in a
+// steady loop at 1.37 GHz and 990 W; a library product of the same codes with
+// one scale for the whole tensor, 418 us at 1.31 GHz. Few tokens are bound by
+// the weights' bytes and 3 to 4 us of start and end: 1 x 8192 x 8192 14.4 us
+// (4.7 TB/s), 16 x 1536 x 2048 4.2 us. What each step gave (8192^3, us): one CTA
+// per tile 673; issuing and scale-loading warps of their own, packed sums 457;
+// pairs in halves 443; a shorter loop 431.
 //
 // Every wait is bounded in time (mbar_wait): one that runs out sets the
 // caller's status word, and the CTA drains its copies and MMAs, frees its TMEM
@@ -79,15 +97,15 @@ struct Cfg {
   static constexpr int kHalves = PAIR ? 2 : 1;
   static constexpr int kUnitN = BN / kHalves;         // columns per MMA
   static constexpr int kBoxQ = kUnitN / kCtas;        // columns that a CTA loads at once
-    static constexpr int kParts = BN >= 64 ? 2 : 1;   // of the columns
+  static constexpr int kParts = BN >= 64 ? 2 : 1;     // of the columns
   static constexpr int kWork = 4 * kParts;            // accumulating warps
   // 256 threads with 128 sums each need more than the 168 registers that 384
-  // threads can have: the first warpgroup (TMA, MMA, an idle warp) gives of its
-  // share. 128 x 56 + 256 x 224 = 384 x 168.
+  // threads can have: the first warpgroup (TMA, MMA, scales) gives of its share.
+  // 128 x 56 + 256 x 224 = 384 x 168.
   static constexpr int kWork0 = 4;                    // first accumulating warp
   static constexpr bool kShift = BN / kParts == 128;
   static constexpr int kThreads = (kWork0 + kWork) * 32;
-  static constexpr int kCols = BN / kParts;          // columns per thread
+  static constexpr int kCols = BN / kParts;           // columns per thread
   static constexpr int NBUF = PAIR ? 2 : 4;           // accumulators (of each half)
   static constexpr uint32_t kTmemCols = NBUF * BN;
   static constexpr uint32_t kTileQ = kHalves * kBoxQ * kBlockK;

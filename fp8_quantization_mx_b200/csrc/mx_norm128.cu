@@ -11,7 +11,12 @@
 //
 // Sums, r, y and the gradients are float; h, y (when asked for) and gh are
 // rounded to x's type once, when stored. Both passes are bound by HBM: each
-// row is read once into registers, 8 elements per lane, and written once.
+// row is read once into registers, 8 elements per lane, and written once. On a
+// B200 with a copy bandwidth of 6.45 TB/s, bf16 with the residual: forward
+// 16387 x 4096 76.9 us (95% of the bytes' time), 8192 x 8192 85 us (86%), 65536
+// x 512 41.7 us (88%), one row of 2048 1.8 us; gradient 16384 x 4096 91.5 us
+// (91%), 65536 x 512 47.2 us (88%), 1999 x 2048 10.6 us (36%: four and a half
+// rows per CTA, then the second kernel's sum of 444 shares of gw).
 
 #include <cuda_runtime.h>
 
@@ -69,12 +74,12 @@ __device__ __forceinline__ float row_rstd(float sum, int64_t cols, float eps) {
 
 // Codes of -ny.
 template <bool E5M2>
-__device__ __forceinline__ uint2 encode8(const float (&ny)[8], const Divisor& d) {
+__device__ __forceinline__ uint2 encode8(const float2 (&ny)[4], const Divisor& d) {
   const float2 s = make_float2(d.s, d.s), ninv = make_float2(d.ninv, d.ninv);
   float2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 x = make_float2(ny[2 * i], ny[2 * i + 1]);
+    float2 x = ny[i];
     if (d.slow) x = __fmul2_rn(x, make_float2(kLift, kLift));
     q[i] = div2(x, s, ninv);
   }
@@ -109,10 +114,10 @@ struct RowThreads {
 };
 
 // NV vectors of 8 elements per thread: the vectors of a tile are 16
-// neighbouring lanes' (four shuffles give its largest magnitude).
+// neighbouring lanes', each of which takes one of the NV tiles' scale.
 // HALF: at most 256 threads with two vectors each, registers for three CTAs of
 // 256 (floats two): 16387 x 4096 took 84.7 us with two of them, 78.2 with
-// three, 92 with four.
+// three, 92 with four (76.9 since the scales are shared out over the lanes).
 template <int DT, bool E5M2, int NV, bool WARP, bool HALF = false>
 __global__ void __launch_bounds__(WARP || NV == 1 || HALF ? 256 : 512,
                                   NV == 1 ? 4 : HALF ? (DT == kFP32 ? 2 : 3) : 1)
@@ -148,51 +153,57 @@ __global__ void __launch_bounds__(WARP || NV == 1 || HALF ? 256 : 512,
   for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     Vec<DT, 8> xn[NV], rn[NV];
     load(row + rt.step, xn, rn);
-    float h[NV][8];
-    float ss[1] = {0.0f};
+    float2 h[NV][4], sq = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = rt.tid + j * rt.nt;
-      float p = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[j][e] = xv[j].get(e) + rv[j].get(e);
-        p = fmaf(h[j][e], h[j][e], p);
+      for (int e = 0; e < 4; ++e) {
+        h[j][e] = __fadd2_rn(xv[j].get2(e), rv[j].get2(e));
+        sq = __ffma2_rn(h[j][e], h[j][e], sq);
       }
-      ss[0] += p;
       if (a.h && i < nvec) {
         Vec<DT, 8> o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.set2(e, h[j][2 * e], h[j][2 * e + 1]);
+        for (int e = 0; e < 4; ++e) o.set2(e, h[j][e].x, h[j][e].y);
         o.store(static_cast<T*>(a.h) + row * a.cols + 8 * i);
       }
     }
+    float ss[1] = {sq.x + sq.y};
     rt.sum(ss, red, par);
-    const float r = -row_rstd(ss[0], a.cols, a.eps);   // y negated, as encode8 takes it
+    const float r = -row_rstd(ss[0], a.cols, a.eps);   // y negated, as div2 takes it
+    float m[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      m[j] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[j][e] = __fmul2_rn(__fmul2_rn(h[j][e], make_float2(r, r)), wv[j].get2(e));
+        m[j] = amax3(m[j], h[j][e].x, h[j][e].y);
+      }
+    }
+    // each lane takes one of its NV tiles' scales
+    float mm = spread_max(m, threadIdx.x & 31);
+#pragma unroll
+    for (int o = NV; o < 16; o <<= 1) mm = amax2(mm, __shfl_xor_sync(~0u, mm, o));
+    const float s = tile_scale<E5M2>(mm, a.pow2);
+    const Divisor mine = divisor(s, mm == 0.0f);
+    {
+      const int j = held_by<NV>(threadIdx.x & 31), i = rt.tid + j * rt.nt;
+      if ((threadIdx.x & 15) < NV && (i & ~15) < nvec) a.scales[(i >> 4) * a.lds + row] = s;
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = rt.tid + j * rt.nt;
-      float y[8], m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = h[j][e] * r * wv[j].get(e);
-        m = amax2(m, y[e]);
-      }
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
-      const float s = tile_scale<E5M2>(m, a.pow2);
-      const uint2 c = encode8<E5M2>(y, divisor(s, m == 0.0f));
+      const uint2 c = encode8<E5M2>(h[j], divisor_of(mine, (threadIdx.x & 16) | lane_of<NV>(j)));
       // codes up to the row's padding to 16 bytes (the vector past the last is 0)
       if (8 * static_cast<int64_t>(i) < pitch)
         *reinterpret_cast<uint2*>(a.codes + row * a.ldc + 8 * i) = c;
-      if (i < nvec) {
-        if ((i & 15) == 0) a.scales[(i >> 4) * a.lds + row] = s;
-        if (a.y) {
-          Vec<DT, 8> o;
+      if (a.y && i < nvec) {
+        Vec<DT, 8> o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o.set2(e, -y[2 * e], -y[2 * e + 1]);
-          o.store(static_cast<T*>(a.y) + row * a.cols + 8 * i);
-        }
+        for (int e = 0; e < 4; ++e) o.set2(e, -h[j][e].x, -h[j][e].y);
+        o.store(static_cast<T*>(a.y) + row * a.cols + 8 * i);
       }
       xv[j] = xn[j];
       rv[j] = rn[j];

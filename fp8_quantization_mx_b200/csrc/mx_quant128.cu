@@ -4,9 +4,9 @@
 //
 // One CTA of 256 threads takes a 128 x 128 piece of x: thread t holds rows
 // 4 (t / 8) .. + 3, columns 16 (t % 8) .. + 15, in registers.
-//   rows     a tile is 8 neighbouring lanes: three shuffles give its largest
-//            magnitude, 16 codes are one 16-byte store, and a lane group's four
-//            scales one 16-byte store of the block-major scale array
+//   rows     a tile is 8 neighbouring lanes, which hold four rows' tiles: each
+//            takes one row's largest magnitude and scale (four shuffles), 16
+//            codes are one 16-byte store
 //   columns  the largest magnitudes of a column over the four rows of a
 //            thread, over the warp's four lane groups (an exchange that halves
 //            the columns held at each step: 12 shuffles where reducing all 16
@@ -16,7 +16,11 @@
 //            conflicts) into 128-byte runs of the transposed codes
 //   block    one scale for the piece; its codes are made once, and the
 //            transposed codes by byte permutes of four rows' words
-// Bound by HBM: x is read once and every code written once.
+// Bound by HBM: x is read once and every code written once. Of bf16, on a B200
+// with a copy bandwidth of 6.45 TB/s: 32768 x 4096 along the rows 63.7 us (99% of
+// the bytes' time), both ways 103 us (82%; about 17 instructions per element by
+// then), 49152 x 2048 in blocks both ways 66.9 us (93%), 4099 x 4096 both ways
+// 17.2 us (61%: 1.8 waves of CTAs, and 3 us of start and end).
 
 #include <cuda_runtime.h>
 
@@ -97,15 +101,16 @@ __device__ __forceinline__ void encode_cols(const Vec<DT, 16> (&v)[4], const flo
 
 // CTAs per SM that the registers are cut for. What hides a piece's load, sums
 // and stores is other CTAs: 32768 x 4096 both ways took 148, 123, 110, 110 us
-// with 2 to 5 of them, rows alone 74, 74, 66, 63; floats spill beyond 3. (One
-// CTA that loads the next piece ahead, at 2 per SM: 152 and 92 us.)
+// with 2 to 5 of them (before the scales were shared out over the lanes: 103
+// with 4); floats spill beyond 3. One CTA that loads the next piece ahead, at 2
+// per SM: 152 us.
 template <int DT>
-constexpr int ctas_per_sm(bool rows, bool cols, bool block) {
-  return DT == kFP32 ? 3 : rows && !cols && !block ? 5 : 4;
+constexpr int ctas_per_sm() {
+  return DT == kFP32 ? 3 : 4;
 }
 
 template <int DT, bool E5M2, bool ROWS, bool COLS, bool BLOCK>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>(ROWS, COLS, BLOCK)) quant128_kernel(const Quant128Args a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>()) quant128_kernel(const Quant128Args a) {
   using T = typename Elem<DT>::T;
   __shared__ __align__(16) uint32_t sh_codes[COLS ? 128 * 32 : 4];
   __shared__ __align__(16) float sh_red[8][BLOCK || !COLS ? 4 : 128];
@@ -155,29 +160,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>(ROWS, COLS, BLOCK)) 
   }
 
   if constexpr (ROWS) {
-    float s4[4] = {};
+    Divisor mine{};
+    if constexpr (!BLOCK) {
+      // a tile is eight lanes; each of them takes one of the four rows' scale
+      float m[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = v[i].amax();
+      float mm = spread_max(m, lane);
+      mm = amax2(mm, __shfl_xor_sync(~0u, mm, 4));
+      const float s = tile_scale<E5M2>(mm, a.pow2);
+      mine = divisor(s, mm == 0.0f);
+      // (lds >= rows rounded up to 4)
+      if (sub < 4 && row0 < a.rows) a.scales[cb * a.lds + row0 + held_by<4>(lane)] = s;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint4 codes;
       if constexpr (BLOCK) {
         codes = rcodes[i];
       } else {
-        float m = v[i].amax();
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
-        const float s = tile_scale<E5M2>(m, a.pow2);
-        const Divisor d = divisor(s, m == 0.0f);
+        const Divisor d = divisor_of(mine, (lane & 24) | lane_of<4>(i));
         codes = d.slow ? encode_row<E5M2, true, DT>(v[i], d) : encode_row<E5M2, false, DT>(v[i], d);
-        s4[i] = s;
       }
       // (a row's 16-byte piece ends within the row's padding to 16 bytes)
       if (row0 + i < a.rows && col0 < a.cols)
         *reinterpret_cast<uint4*>(a.codes + (row0 + i) * a.ldc + col0) = codes;
     }
-    // four rows' scales; lds >= rows rounded up to 4
-    if (!BLOCK && sub == 0 && row0 < a.rows)
-      *reinterpret_cast<float4*>(a.scales + cb * a.lds + row0) =
-          make_float4(s4[0], s4[1], s4[2], s4[3]);
   }
 
   if constexpr (COLS) {

@@ -49,11 +49,53 @@ __device__ __forceinline__ float amax2(float a, float b) {
   return r;
 }
 
+// max(|a|, |b|, |c|), NaN kept.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// N (1, 2 or 4) maxima that each of a group of lanes holds a part of, one per
+// lane: every step exchanges half of those held with a neighbour (N - 1
+// shuffles where reducing all N in every lane takes N log N). Lane l then holds
+// part of maximum held_by<N>(l); what is left is to take the maximum over lanes
+// a multiple of N apart. lane_of<N>(j) is the lane of the first N that holds j.
+template <int N>
+__device__ __forceinline__ int held_by(int lane) {
+  return N == 4 ? (lane & 1) << 1 | (lane >> 1 & 1) : N == 2 ? lane & 1 : 0;
+}
+template <int N>
+__device__ __forceinline__ int lane_of(int j) {
+  return N == 4 ? j >> 1 | (j & 1) << 1 : j;
+}
+template <int N>
+__device__ __forceinline__ float spread_max(const float (&m)[N], int lane) {
+  static_assert(N == 1 || N == 2 || N == 4, "maxima");
+  if constexpr (N == 1) {
+    return m[0];
+  } else if constexpr (N == 2) {
+    const bool odd = lane & 1;
+    return amax2(odd ? m[1] : m[0], __shfl_xor_sync(~0u, odd ? m[0] : m[1], 1));
+  } else {
+    const bool odd = lane & 1, two = lane & 2;
+    const float a = amax2(odd ? m[2] : m[0], __shfl_xor_sync(~0u, odd ? m[0] : m[2], 1));
+    const float b = amax2(odd ? m[3] : m[1], __shfl_xor_sync(~0u, odd ? m[1] : m[3], 1));
+    return amax2(two ? b : a, __shfl_xor_sync(~0u, two ? a : b, 2));
+  }
+}
+
 // The scale of a tile from its largest magnitude.
 template <bool E5M2>
 __device__ __forceinline__ float tile_scale(float amax, bool pow2) {
   if (!(amax < __int_as_float(0x7f800000))) return __int_as_float(0x7fc00000);
-  if (!pow2) return fmaxf(__fdiv_rn(amax, max_code<E5M2>()), kTinyScale);
+  if (!pow2) {
+    // amax / maxv correctly rounded, as div2 does it (below 2^-126, where the
+    // remainder is not exact, the floor decides)
+    constexpr float c = 1.0f / max_code<E5M2>();
+    const float q = amax * c;
+    return fmaxf(fmaf(fmaf(q, -max_code<E5M2>(), amax), c, q), kTinyScale);
+  }
   // maxv = 1.75 2^top: the exponent of amax less `top`, one more where the
   // significand is above 1.75 (in biased exponents, at least 1)
   constexpr int kTop = E5M2 ? 15 : 8;
@@ -91,6 +133,12 @@ __device__ __forceinline__ Divisor divisor(float s, bool zero) {
     d.ninv *= 1.0f / kLift;
   }
   return d;
+}
+
+// Lane src's divisor in every lane.
+__device__ __forceinline__ Divisor divisor_of(const Divisor& d, int src) {
+  const float s = __shfl_sync(~0u, d.slow ? -d.s : d.s, src);   // (s > 0 or NaN)
+  return {fabsf(s), __shfl_sync(~0u, d.ninv, src), s < 0.0f};
 }
 
 // Two codes: lo in bits 0-7, hi in bits 8-15.
@@ -181,6 +229,7 @@ struct Vec {
       return __uint_as_float(w[i]);
     }
   }
+  __device__ __forceinline__ float2 get2(int i) const { return make_float2(get(2 * i), get(2 * i + 1)); }
   // Elements 2i and 2i + 1, negated.
   __device__ __forceinline__ float2 neg2(int i) const {
     if constexpr (DT == kFP32) {
@@ -196,7 +245,7 @@ struct Vec {
     if constexpr (DT == kFP32) {
       float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = amax2(m, get(i));
+      for (int i = 0; i < N; i += 2) m = amax3(m, get(i), get(i + 1));
       return m;
     } else {
       uint32_t m = w[0];
