@@ -287,11 +287,12 @@ __device__ __forceinline__ void add_split(const Smem<C>& sm, const Gemm128Args& 
 // One tile of D from the sums in registers (rows on the row side): a warp
 // stages 32 rows of kStgRow bytes in its own shared memory, so that a row
 // leaves as full 16-byte lanes of one run.
-template <class C, int ES>
+template <class C, int ES, bool VEC>
 __device__ __forceinline__ void store_tile(const Smem<C>& sm, const Gemm128Args& g,
                                            const float (&acc)[C::kCols], int64_t p0,
                                            int64_t q0, int warp, int lane) {
   constexpr int kChunk = (C::kStgRow / ES < C::kCols) ? C::kStgRow / ES : C::kCols;
+  static_assert(kChunk <= 32, "a lane per column");
   constexpr int NJ = kChunk * ES / 16;          // 16-byte units per row
   constexpr int kPer = 16 / ES;                 // elements per unit
   constexpr int kRowsPer = 32 / NJ;             // rows per store instruction
@@ -313,26 +314,31 @@ __device__ __forceinline__ void store_tile(const Smem<C>& sm, const Gemm128Args&
       *reinterpret_cast<uint4*>(stg + lane * (NJ * 16) + ((j ^ (lane & (NJ - 1))) * 16)) = v;
     }
     __syncwarp();
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < NJ; ++i) {
-      const int r = i * kRowsPer + lane / NJ, j = lane % NJ;
-      const uint4 v =
-          *reinterpret_cast<const uint4*>(stg + r * (NJ * 16) + ((j ^ (r & (NJ - 1))) * 16));
-      const int64_t row = row0 + r, col = colh + c0 + j * kPer;
-      if (row < g.P && col < g.Q) {
-        uint8_t* d = g.d + (row * g.ldd + col) * ES;
-        if (g.vec && col + kPer <= g.Q) {
-          *reinterpret_cast<uint4*>(d) = v;
-        } else {
-          const uint32_t* w = &v.x;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e)
-            if (col + e < g.Q) {
-              if constexpr (ES == 2)
-                reinterpret_cast<uint16_t*>(d)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
-              else
-                reinterpret_cast<uint32_t*>(d)[e] = w[e];
-            }
+      for (int i = 0; i < NJ; ++i) {
+        const int r = i * kRowsPer + lane / NJ, j = lane % NJ;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(stg + r * (NJ * 16) + ((j ^ (r & (NJ - 1))) * 16));
+        const int64_t row = row0 + r, col = colh + c0 + j * kPer;
+        // (N is then a multiple of kPer)
+        if (row < g.P && col < g.Q)
+          *reinterpret_cast<uint4*>(g.d + (row * g.ldd + col) * ES) = v;
+      }
+    } else {
+      // rows at any alignment: neighbouring lanes write neighbouring elements
+      // (a lane with 16 bytes of its own, element by element, took 30 us for
+      // 7135 x 543 x 1557)
+      const int c = lane % kChunk;
+      const int64_t col = colh + c0 + c;
+#pragma unroll 4
+      for (int r = lane / kChunk; r < 32; r += 32 / kChunk) {
+        const uint8_t* at = stg + r * (NJ * 16) + (((c / kPer) ^ (r & (NJ - 1))) * 16) + c % kPer * ES;
+        const int64_t row = row0 + r;
+        if (row < g.P && col < g.Q) {
+          uint8_t* d = g.d + (row * g.ldd + col) * ES;
+          if constexpr (ES == 2) *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(at);
+          else *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(at);
         }
       }
     }
@@ -361,7 +367,9 @@ __device__ __forceinline__ void store_tile_swapped(const Gemm128Args& g,
   }
 }
 
-template <class C>
+// VEC: rows of D start on 16-byte boundaries (an instance of its own, since the
+// other stores' code beside these made the K-blocks' loop 10% slower).
+template <class C, bool VEC>
 __global__ void __launch_bounds__(C::kThreads, 1)
     gemm128_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const Gemm128Args g) {
@@ -703,8 +711,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       } else if constexpr (C::SWAP) {
         store_tile_swapped<C>(g, acc, p0, q0, warp, lane);
       } else {
-        if (g.out_fp32) store_tile<C, 4>(sm, g, acc, p0, q0, warp, lane);
-        else store_tile<C, 2>(sm, g, acc, p0, q0, warp, lane);
+        if (g.out_fp32) store_tile<C, 4, VEC>(sm, g, acc, p0, q0, warp, lane);
+        else store_tile<C, 2, VEC>(sm, g, acc, p0, q0, warp, lane);
       }
     }
     tc::tc_fence_before();
@@ -774,9 +782,9 @@ cudaError_t device_sms(int* dev, int* sms) {
   return e;
 }
 
-template <class C>
-cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream_t st) {
-  auto kern = gemm128_kernel<C>;
+template <class C, bool VEC>
+cudaError_t launch_vec(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream_t st) {
+  auto kern = gemm128_kernel<C, VEC>;
   // the kernel's shared-memory limit, set once per device
   static std::atomic<uint64_t> ready{0};
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
@@ -807,6 +815,13 @@ cudaError_t launch(const Gemm128& u, Gemm128Args g, int dev, int sms, cudaStream
   const int64_t most = g.split > 1 ? tiles : sms / cluster;
   const unsigned grid = static_cast<unsigned>((tiles < most ? tiles : most) * cluster);
   return launch_dependent(kern, dim3(grid), dim3(C::kThreads), C::kSmem, st, cluster, tmP, tmQ, g);
+}
+
+template <class C>
+cudaError_t launch(const Gemm128& u, const Gemm128Args& g, int dev, int sms, cudaStream_t st) {
+  if constexpr (!C::SWAP)   // (swapped tiles are stored element by element)
+    if (!g.vec) return launch_vec<C, false>(u, g, dev, sms, st);
+  return launch_vec<C, true>(u, g, dev, sms, st);
 }
 
 }  // namespace
@@ -868,7 +883,7 @@ cudaError_t device_clusters(int dev, int* c4, int* c8) {
   int v = known[dev].load(std::memory_order_relaxed);
   if (v == 0) {
     using C = Cfg<128, false, false, false, 4>;
-    auto kern = gemm128_kernel<C>;
+    auto kern = gemm128_kernel<C, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(C::kSmem));
     int n[2] = {0, 0};

@@ -281,6 +281,64 @@ __global__ void __launch_bounds__(256) norm128_any_kernel(const NormArgs a) {
   }
 }
 
+// The same for rows of up to 32 NJ (at most 1024) columns: a warp per row, eight
+// rows per CTA; four neighbouring elements of a lane are a tile's.
+template <int DT, bool E5M2, int NJ>
+__global__ void __launch_bounds__(256) norm128_any_warp_kernel(const NormArgs a) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  const int lane = threadIdx.x & 31;
+  dependent_launch();
+  dependent_wait();
+  const int64_t row = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const int cols = static_cast<int>(a.cols), pitch = (cols + 15) & ~15;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
+  const T* w = static_cast<const T*>(a.weight);
+  float h[NJ], wv[NJ], ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int c = lane + 32 * j;
+    h[j] = c < cols ? E::to_float(x[c]) + (res ? E::to_float(res[c]) : 0.0f) : 0.0f;
+    wv[j] = c < cols ? E::to_float(w[c]) : 0.0f;
+    ss = fmaf(h[j], h[j], ss);
+  }
+  const float r = row_rstd(warp_sum(ss), a.cols, a.eps);
+#pragma unroll
+  for (int t = 0; t < NJ / 4; ++t) {
+    if (t * 128 >= cols) break;
+    float y[4], m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = lane + 32 * (4 * t + j);
+      y[j] = c < cols ? h[4 * t + j] * r * wv[4 * t + j] : 0.0f;
+      m = amax2(m, y[j]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = amax2(m, __shfl_xor_sync(~0u, m, o));
+    const float s = tile_scale<E5M2>(m, a.pow2);
+    const Divisor d = divisor(s, m == 0.0f);
+    if (lane == 0) a.scales[t * a.lds + row] = s;
+    const float k = d.slow ? -kLift : -1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 q = div2(make_float2(y[j] * k, y[j + 1] * k), make_float2(d.s, d.s),
+                            make_float2(d.ninv, d.ninv));
+      const uint32_t codes = enc2<E5M2>(q.x, q.y);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = lane + 32 * (4 * t + j + e);
+        if (c < pitch) a.codes[row * a.ldc + c] = static_cast<uint8_t>(codes >> (8 * e));
+        if (c < cols) {
+          if (a.h) static_cast<T*>(a.h)[row * a.cols + c] = E::from_float(h[4 * t + j + e]);
+          if (a.y) static_cast<T*>(a.y)[row * a.cols + c] = E::from_float(y[j + e]);
+        }
+      }
+    }
+  }
+}
+
 // --------------------------------------------------------------- gradient --
 
 struct NormBwdArgs {
@@ -430,25 +488,27 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
 
 // Any number of columns at any alignment, element tid + 256 j in thread tid: up
 // to 256 NJ columns in registers; beyond, a row is read twice and a thread adds
-// to its columns of the CTA's share of gw in memory.
-template <int DT, int NJ>
+// to its columns of the CTA's share of gw in memory. WARP: up to 32 NJ columns,
+// a warp per row.
+template <int DT, int NJ, bool WARP>
 __global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(const NormBwdArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   __shared__ float red[2][64];
   dependent_launch();
   dependent_wait();
-  const int tid = threadIdx.x;
+  const RowThreads<WARP> rt;
+  const int tid = rt.tid, nt = rt.nt;
   const T* w = static_cast<const T*>(a.weight);
   float* part = a.part + blockIdx.x * a.cols;
   float gw[NJ], wv[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     gw[j] = 0.0f;
-    wv[j] = tid + 256 * j < a.cols ? E::to_float(w[tid + 256 * j]) : 0.0f;
+    wv[j] = tid + nt * j < a.cols ? E::to_float(w[tid + nt * j]) : 0.0f;
   }
   int par = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
+  for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
     const T* hh = static_cast<const T*>(a.h) + row * a.cols;
     const T* gres = a.gres ? static_cast<const T*>(a.gres) + row * a.cols : nullptr;
@@ -456,38 +516,54 @@ __global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(cons
     float g[NJ], h[NJ], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int64_t c = tid + 256 * j;
+      const int64_t c = tid + nt * j;
       g[j] = c < a.cols ? E::to_float(gy[c]) : 0.0f;
       h[j] = c < a.cols ? E::to_float(hh[c]) : 0.0f;
       s[0] = fmaf(h[j], h[j], s[0]);
       s[1] = fmaf(g[j] * wv[j], h[j], s[1]);
     }
-    for (int64_t c = tid + 256 * NJ; c < a.cols; c += 256) {
+    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += 256) {
       const float v = E::to_float(hh[c]);
       s[0] = fmaf(v, v, s[0]);
       s[1] = fmaf(E::to_float(gy[c]) * E::to_float(w[c]), v, s[1]);
     }
-    block_sum(s, red[par]);
+    rt.sum(s, red, par);
     const float r = row_rstd(s[0], a.cols, a.eps);
     const float m = __fdiv_rn(s[1] * r, static_cast<float>(a.cols));
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int64_t c = tid + 256 * j;
+      const int64_t c = tid + nt * j;
       const float n = h[j] * r;
       gw[j] = fmaf(g[j], n, gw[j]);
       if (c < a.cols)
         gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), gres ? E::to_float(gres[c]) : 0.0f));
     }
-    for (int64_t c = tid + 256 * NJ; c < a.cols; c += 256) {
+    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += 256) {
       const float n = E::to_float(hh[c]) * r, v = E::to_float(gy[c]);
       part[c] = fmaf(v, n, row == blockIdx.x ? 0.0f : part[c]);
       gh[c] = E::from_float(
           fmaf(r, fmaf(-n, m, v * E::to_float(w[c])), gres ? E::to_float(gres[c]) : 0.0f));
     }
   }
+  if constexpr (WARP) {
+    __shared__ float sh_part[8][32];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    if (tid + 256 * j < a.cols) part[tid + 256 * j] = gw[j];
+    for (int j = 0; j < NJ; ++j) {
+      if (j) __syncthreads();
+      sh_part[threadIdx.x >> 5][tid] = gw[j];
+      __syncthreads();
+      if (threadIdx.x < 32 && tid + 32 * j < a.cols) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) sum += sh_part[v][tid];
+        part[tid + 32 * j] = sum;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (tid + 256 * j < a.cols) part[tid + 256 * j] = gw[j];
+  }
 }
 
 // gw[c] = sum of the CTAs' shares, in an order that depends on their number
@@ -544,6 +620,13 @@ int64_t grid_for(const Shape& s, int64_t rows, int sms, int threads) {
 
 template <int DT, bool E5M2>
 cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
+  // (a few rows: a CTA each, since what counts is one row's time)
+  if (!vec && a.cols <= 1024 && a.rows > 4 * sms) {
+    const auto kern = a.cols <= 256   ? norm128_any_warp_kernel<DT, E5M2, 8>
+                      : a.cols <= 512 ? norm128_any_warp_kernel<DT, E5M2, 16>
+                                      : norm128_any_warp_kernel<DT, E5M2, 32>;
+    return launch_dependent(kern, dim3(static_cast<unsigned>((a.rows + 7) / 8)), dim3(256), 0, st, 1, a);
+  }
   if (!vec) {
     const auto kern = a.cols <= 1024   ? norm128_any_kernel<DT, E5M2, 4>
                       : a.cols <= 2048 ? norm128_any_kernel<DT, E5M2, 8>
@@ -568,16 +651,22 @@ cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
 template <int DT>
 cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaStream_t st) {
   const Shape s = shape_of(a.cols / 8, a.rows, sms);
-  // (the kernels for any size: 256 threads, four CTAs per SM up to 2048 columns)
-  const int64_t any = (a.cols <= 2048 ? 4 : 2) * sms;
+  // The kernels for any size: 256 threads; many rows of up to 512 columns a warp
+  // each (5324 x 355: 14.4 us, 18.1 with a CTA each; at 1001 columns its
+  // registers leave one CTA per SM and it takes 63 us for 27).
+  const bool warp = a.cols <= 512 && a.rows > 4 * sms;
+  const int nj = warp ? (a.cols <= 256 ? 8 : 16) : a.cols <= 1024 ? 4 : a.cols <= 2048 ? 8 : 16;
+  const int64_t any = (nj <= 8 ? 4 : 2) * sms;
+  const int64_t any_rows = warp ? (a.rows + 7) / 8 : a.rows;
   int64_t grid = vec ? grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512)
-                     : (a.rows < any ? a.rows : any);
+                     : (any_rows < any ? any_rows : any);
   if (grid > kNormParts) grid = kNormParts;
   cudaError_t e;
   if (!vec) {
-    const auto kern = a.cols <= 1024   ? norm_bwd_any_kernel<DT, 4>
-                      : a.cols <= 2048 ? norm_bwd_any_kernel<DT, 8>
-                                       : norm_bwd_any_kernel<DT, 16>;
+    const auto kern = warp ? (nj == 8 ? norm_bwd_any_kernel<DT, 8, true> : norm_bwd_any_kernel<DT, 16, true>)
+                           : (nj == 4   ? norm_bwd_any_kernel<DT, 4, false>
+                              : nj == 8 ? norm_bwd_any_kernel<DT, 8, false>
+                                        : norm_bwd_any_kernel<DT, 16, false>);
     e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, 1, a);
   } else {
     const auto kern = s.warp ? (s.nv == 1   ? norm_bwd_kernel<DT, 1, true>

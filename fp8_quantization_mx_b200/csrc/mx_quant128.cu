@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>()) quant128_kernel(c
   const int64_t rb = blockIdx.x / a.nbc, cb = blockIdx.x % a.nbc;
   const int64_t row0 = rb * 128 + 4 * g, col0 = cb * 128 + 16 * sub;
 
+  // a shifted load reads up to 15 bytes around its elements: within x only
+  const T* first = static_cast<const T*>(a.x) + 16;
+  const T* past = static_cast<const T*>(a.x) + (a.rows - 1) * a.ldx + a.cols;
   Vec<DT, 16> v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -133,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>()) quant128_kernel(c
       v[i].zero();
     else if (a.vec && col0 + 16 <= a.cols)
       v[i].load(p);
+    else if (col0 + 16 <= a.cols && p >= first && p + 32 <= past)
+      v[i].load_shifted(p);
     else
       v[i].load_some(p, a.cols - col0);
   }

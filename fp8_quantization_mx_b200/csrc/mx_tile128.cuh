@@ -205,6 +205,31 @@ struct Vec {
           : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
           : "l"(reinterpret_cast<const char*>(p) + 4 * i));
   }
+  // All N elements at any alignment of an element, from aligned 16-byte loads:
+  // the bytes from p rounded down to 16 up to p + N elements rounded up are read.
+  __device__ __forceinline__ void load_shifted(const typename E::T* p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t off = at & 15;
+    const char* q = reinterpret_cast<const char*>(at - off);
+    uint32_t t[kWords + 4];
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+          : "=r"(t[i]), "=r"(t[i + 1]), "=r"(t[i + 2]), "=r"(t[i + 3])
+          : "l"(q + 4 * i));
+#pragma unroll
+    for (int i = kWords; i < kWords + 4; ++i) t[i] = 0;
+    if (off)
+      asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+          : "=r"(t[kWords]), "=r"(t[kWords + 1]), "=r"(t[kWords + 2]), "=r"(t[kWords + 3])
+          : "l"(q + 4 * kWords));
+#pragma unroll
+    for (int i = 0; i < kWords + 2; ++i) t[i] = (off & 8) ? t[i + 2] : t[i];
+#pragma unroll
+    for (int i = 0; i < kWords + 1; ++i) t[i] = (off & 4) ? t[i + 1] : t[i];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(t[i], t[i + 1], (off & 3) * 8);
+  }
   // The first n elements, one at a time; the rest 0.
   __device__ __forceinline__ void load_some(const typename E::T* p, int64_t n) {
     zero();
