@@ -264,23 +264,36 @@ __device__ __forceinline__ void add_split(const Smem<C>& sm, const Gemm128Args& 
   constexpr int kUnits = kMajor * L / 4 / SPLIT;
   const int64_t rows = C::SWAP ? g.Q : g.P, cols = C::SWAP ? g.P : g.Q;
   const int64_t r0 = C::SWAP ? q0 : p0, c0 = C::SWAP ? p0 : q0;
-  for (int u = threadIdx.x - C::kWork0 * 32; u < kUnits; u += C::kWork * 32) {
-    const int at = static_cast<int>(rank) * kUnits + u;
-    const int major = at / (L / 4), minor = at % (L / 4) * 4;
-    if (r0 + major >= rows || c0 + minor >= cols) continue;
-    const uint32_t a = sm.ring + part_at<L>(major, minor);
-    float4 v[SPLIT];
+  // several units' loads in flight: one after the other they took 3 us of a
+  // 128-wide tile split in two
+  constexpr int kThreads = C::kWork * 32;
+  constexpr int kAtOnce = SPLIT == 8 ? 2 : 4;
+  for (int u0 = threadIdx.x - C::kWork0 * 32; u0 < kUnits; u0 += kThreads * kAtOnce) {
+    float4 v[kAtOnce][SPLIT];
 #pragma unroll
-    for (int r = 0; r < SPLIT; ++r) v[r] = ld_cluster4(tc::mapa(a, r));
-    float4 s = v[0];
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int u = u0 + i * kThreads < kUnits ? u0 + i * kThreads : 0;
+      const int at = static_cast<int>(rank) * kUnits + u;
+      const uint32_t a = sm.ring + part_at<L>(at / (L / 4), at % (L / 4) * 4);
 #pragma unroll
-    for (int r = 1; r < SPLIT; ++r) {
-      s.x += v[r].x;
-      s.y += v[r].y;
-      s.z += v[r].z;
-      s.w += v[r].w;
+      for (int r = 0; r < SPLIT; ++r) v[i][r] = ld_cluster4(tc::mapa(a, r));
     }
-    store4(g, r0 + major, c0 + minor, cols - c0 - minor, s);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int u = u0 + i * kThreads;
+      const int at = static_cast<int>(rank) * kUnits + u;
+      const int major = at / (L / 4), minor = at % (L / 4) * 4;
+      if (u >= kUnits || r0 + major >= rows || c0 + minor >= cols) continue;
+      float4 s = v[i][0];
+#pragma unroll
+      for (int r = 1; r < SPLIT; ++r) {
+        s.x += v[i][r].x;
+        s.y += v[i][r].y;
+        s.z += v[i][r].z;
+        s.w += v[i][r].w;
+      }
+      store4(g, r0 + major, c0 + minor, cols - c0 - minor, s);
+    }
   }
 }
 
@@ -694,7 +707,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (!C::PAIR && g.split > 1) {
         // the ring is idle: every K-block loaded has been multiplied. (The
-        // generic writes below follow the MMAs' reads through tfull.)
+        // generic writes below follow the MMAs' reads through `done`.)
 #pragma unroll
         for (int i = 0; i < C::kCols; i += 4) {
           const float4 v = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
@@ -826,10 +839,11 @@ cudaError_t launch(const Gemm128& u, const Gemm128Args& g, int dev, int sms, cud
 
 }  // namespace
 
-// The cheapest cut by a model of the time: waves of clusters times the K-blocks
-// of a CTA times a K-block's time, plus what joining a split costs (more for
-// wide tiles, whose partial sums cross the cluster). Its figures are measured
-// (us), and it chose within 6% of the best cut at all but a few of 80 sizes:
+// The cheapest cut by a model of the time: waves of clusters, each the K-blocks
+// of a CTA times a K-block's time, a start and end, and what joining a split
+// costs (more for wide tiles, whose partial sums cross the cluster). Its figures
+// (us) are fitted to measurements of every cut at 120 sizes, of which it chose
+// the best or one 1% slower on average, 14% at worst (2048 x 511 x 6000):
 //   a tile that is finer than needed loses to its number of waves, one that is
 //   coarser leaves SMs idle: 128 x 8192 x 4096 takes 10.6 us in 64-wide tiles,
 //   13.1 in 128-wide ones on two CTAs each, 18 in pairs' tiles; 512 x 8192 x
@@ -844,9 +858,9 @@ Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int
     double kb_block, kb_tile, tail;   // per K-block with block / tile weights, per wave
   };
   static constexpr Cut kCuts[] = {
-      {16, 1, 0.22, 0.22, 0.3}, {32, 1, 0.225, 0.225, 0.4}, {64, 1, 0.25, 0.25, 0.6},
-      {64, 0, 0.19, 0.25, 0.3}, {128, 0, 0.27, 0.36, 1.0},  {256, 0, 0.41, 0.62, 1.5}};
-  static constexpr double kJoin[] = {0.0, 0.5, 1.0, 1.3};
+      {16, 1, 0.22, 0.215, 1.5}, {32, 1, 0.25, 0.26, 1.7}, {64, 1, 0.305, 0.31, 1.8},
+      {64, 0, 0.21, 0.29, 1.9},  {128, 0, 0.31, 0.4, 1.5}, {256, 0, 0.37, 0.62, 3.75}};
+  static constexpr double kJoin[] = {0.0, 0.7, 1.2, 1.6};
   const int64_t nk = (K + 127) / 128;
   Plan128 best{};
   double best_t = 0.0;
@@ -863,8 +877,8 @@ Plan128 plan_gemm128(int64_t M, int64_t N, int64_t K, bool b_block, int sms, int
       const int64_t waves = (tiles + slots - 1) / slots;
       const double t = static_cast<double>(waves) *
                            (static_cast<double>((nk + split - 1) / split) *
-                                (b_block ? c.kb_block : c.kb_tile) + c.tail) +
-                       (i ? kJoin[i] + 0.015 * c.bn : 0.0);
+                                (b_block ? c.kb_block : c.kb_tile) +
+                            c.tail + (i ? kJoin[i] + 0.022 * c.bn : 0.0));
       if (best_t == 0.0 || t < best_t) {
         best = {c.bn, c.swap, split};
         best_t = t;
@@ -957,9 +971,9 @@ Gemm128 part_of(const Gemm128& u, int64_t m0, int64_t M, int64_t n0, int64_t N) 
 // Sizes a little over a multiple of 256 cost whole tiles, at times a whole wave
 // of them: rows and columns past the multiple are then products of their own,
 // if by the model that is cheaper (4099 x 2056 x 8192: one wave of three, 81 ->
-// 70 us). A further launch on the stream costs 3 us.
+// 70 us). A further launch on the stream costs 1.7 us beyond its own time.
 cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st) {
-  constexpr double kLaunch = 3.0;
+  constexpr double kLaunch = 1.7;
   int dev = 0, sms = 0, c4 = 0, c8 = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;

@@ -267,7 +267,11 @@ GEMM_SHAPES = [(1, 128, 128), (1, 1, 1), (7, 130, 96), (16, 1536, 2048), (17, 39
                (1, 32, 1289), (2, 33, 1168), (129, 4968, 84), (135, 160, 2563), (257, 149, 3686),
                (265, 336, 4927), (284, 135, 2597), (292, 399, 1697), (340, 386, 1466), (397, 264, 1831),
                (548, 949, 3685), (685, 343, 3379), (775, 283, 2005), (900, 3656, 78), (1265, 536, 5790),
-               (1329, 1916, 5019), (1860, 1245, 424), (2838, 1865, 4884)]
+               (1329, 1916, 5019), (1860, 1245, 424), (2838, 1865, 4884),
+               (288, 16, 6143), (1201, 17, 2623), (2054, 16, 2489), (33, 1467, 6685), (2417, 70, 3183),
+               (1431, 133, 7695), (1200, 21, 2222), (2808, 17, 1969), (2856, 138, 399),
+               (2564, 132, 520), (697, 145, 7973), (37, 4784, 5026), (72, 5302, 7758),
+               (137, 5359, 7915)]
 
 
 @pytest.mark.parametrize("block", [True, False])
