@@ -85,7 +85,7 @@ cudaError_t clear_padding(uint8_t* scales, int64_t rows, int64_t cols, int flags
 
 extern "C" {
 
-int mx_version(void) { return (1 << 16) | 0; }
+int mx_version(void) { return (1 << 16) | 1; }
 
 const char* mx_status_string(int status) {
   switch (status) {

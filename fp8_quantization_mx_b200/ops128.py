@@ -200,7 +200,9 @@ def quantize128(x: torch.Tensor, format: int = E4M3, block: bool = False, direct
     * ``"cols"``: ``(codes_t [cols, rows], scales_t)``, the same of x transposed;
     * ``"both"``: ``(codes, scales, codes_t, scales_t)``, from one read of x.
 
-    ``pow2``: power-of-two scales. ``out`` may supply the two or four tensors."""
+    ``pow2``: power-of-two scales. ``out`` may supply the two or four tensors;
+    a row of its codes is written up to a multiple of 16 bytes, a tile's scales
+    up to a multiple of 4 rows."""
     _fp8_format(format)
     if direction not in _DIRECTIONS:
         raise ValueError("direction must be 'rows', 'cols' or 'both'")
@@ -452,6 +454,8 @@ def linear128(x: torch.Tensor, weight: torch.Tensor, grad_format: int = E4M3) ->
     ``FP8Linear128``). x bfloat16 [..., K], weight bfloat16 [N, K];
     ``grad_format``: the output gradient's FP8 format."""
     _layer_inputs(x=x, weight=weight)
+    if not torch.is_grad_enabled():   # nothing is kept for a backward pass
+        x, weight = x.detach(), weight.detach()
     y = FP8Linear128.apply(x.reshape(-1, x.shape[-1]), weight, grad_format)
     return y.view(*x.shape[:-1], weight.shape[0])
 
@@ -466,6 +470,9 @@ def rms_norm_linear128(x: torch.Tensor, norm_weight: torch.Tensor, weight: torch
     shape = x.shape
     if residual is not None and residual.shape != shape:
         raise ValueError(f"residual must be {list(shape)}, got {list(residual.shape)}")
+    if not torch.is_grad_enabled():   # nothing is kept for a backward pass
+        x, norm_weight, weight = x.detach(), norm_weight.detach(), weight.detach()
+        residual = None if residual is None else residual.detach()
     res = None if residual is None else residual.reshape(-1, shape[-1]).contiguous()
     out, h = FP8NormLinear128.apply(x.reshape(-1, shape[-1]), res, norm_weight, weight, eps,
                                     grad_format)

@@ -311,12 +311,12 @@ int mx_quant_gemm_noalloc(const void* a_bf16, int scaling, const void* b_codes,
  * and code * s is the value. A zero tile has s = 2^-126 and codes +-0.
  *
  * Layouts. Codes: [rows, ld] bytes, ld a multiple of 16 and at least cols;
- * the quantizers write each row's bytes up to cols rounded up to 16 (zeros
- * past cols), nothing beyond. Tile scales are block-major: the scale of row r,
- * tile j sits at scales[j * lds + r], lds a multiple of 4 and at least rows
- * rounded up to 4 (the up to 3 floats past the last row may be written, and
- * are read but not used). Block scales: row-major [ceil(rows/128),
- * ceil(cols/128)], contiguous.
+ * the quantizers write each row's bytes up to cols rounded up to 16 (past
+ * cols zeros, or NaN where the last tile is), nothing beyond. Tile scales are
+ * block-major: the scale of row r, tile j sits at scales[j * lds + r], lds a
+ * multiple of 4 and at least rows rounded up to 4 (the up to 3 floats past the
+ * last row may be written, and are read but not used). Block scales: row-major
+ * [ceil(rows/128), ceil(cols/128)], contiguous.
  * Alignment: codes and tile scales 16 bytes, D 16 bytes, workspace 16 bytes,
  * everything else its element. Rows that start on 16-byte boundaries are read
  * fastest. MX_ERR_SHAPE: a pitch (ld...) too small or not such a multiple.

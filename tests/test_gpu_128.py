@@ -607,3 +607,36 @@ def test_offsets_beyond_32_bits(mx, cuda):
     del nc, ns, c, s
     gh, _ = mx.rms_norm_bwd(x, h, w)
     assert torch.equal(gh[-tail:], mx.rms_norm_bwd(last, mh, w)[0])
+
+
+def test_padding_of_rows_is_zero_or_nan(mx, cuda):
+    """Past cols a row's codes are zeros up to a multiple of 16, and NaN where
+    the row's last tile holds one."""
+    for cols in (24, 20):   # the norm's two kinds of kernels
+        x = values(40, cols, torch.bfloat16, 5)
+        x[3, 1] = float("nan")
+        x[5] = 0.0
+        x = x.to(cuda)
+        for codes in (mx.quantize128(x)[0], mx.quantize128(x, direction="both")[0],
+                      mx.rms_norm_quantize(x, torch.ones_like(x[0]), eps=0.0)[0]):
+            pad = codes.as_strided((40, 32 - cols), (32, 1), cols).cpu()
+            bad = codes[:, 0].cpu() == 0x7F
+            assert bad[3] and bad.sum() <= 2
+            assert (pad[bad] == 0x7F).all() and (pad[~bad] == 0).all()
+
+
+def test_layers_without_gradients_keep_nothing(mx, cuda, monkeypatch):
+    """Under no_grad the layers make no transposed operands, whatever their
+    inputs require; the results are the same."""
+    from fp8_quantization_mx_b200 import ops128
+    x, r, nw, w = [t.requires_grad_() for t in layer_inputs(64, 256, 384)]
+    y, (z, h) = mx.linear128(x, w), mx.rms_norm_linear128(x, nw, w, r)
+    made, quantize = [], ops128.quantize128
+    monkeypatch.setattr(ops128, "quantize128",
+                        lambda *a, direction="rows", **k: (made.append(direction),
+                                                           quantize(*a, direction=direction, **k))[1])
+    with torch.no_grad():
+        y0, (z0, h0) = mx.linear128(x, w), mx.rms_norm_linear128(x, nw, w, r)
+    assert made == ["rows"] * 3
+    assert torch.equal(y, y0) and torch.equal(z, z0) and torch.equal(h, h0)
+    assert not (y0.requires_grad or z0.requires_grad or h0.requires_grad)
