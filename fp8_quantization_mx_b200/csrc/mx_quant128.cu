@@ -18,9 +18,9 @@
 //            transposed codes by byte permutes of four rows' words
 // Bound by HBM: x is read once and every code written once. Of bf16, on a B200
 // with a copy bandwidth of 6.45 TB/s: 32768 x 4096 along the rows 63.7 us (99% of
-// the bytes' time), both ways 103 us (82%; about 17 instructions per element by
-// then), 49152 x 2048 in blocks both ways 66.9 us (93%), 4099 x 4096 both ways
-// 17.2 us (61%: 1.8 waves of CTAs, and 3 us of start and end).
+// the bytes' time), both ways 103 us (82%; 18.6 instructions per element),
+// 49152 x 2048 in blocks both ways 66 us (95%), 4099 x 4096 both ways 17 us
+// (62%: 1.8 waves of CTAs, and 3 us of start and end).
 
 #include <cuda_runtime.h>
 
@@ -197,11 +197,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<DT>()) quant128_kernel(c
     if constexpr (BLOCK) {
 #pragma unroll
       for (int c4 = 0; c4 < 4; ++c4) {
-        const uint32_t* r[4] = {&rcodes[0].x, &rcodes[1].x, &rcodes[2].x, &rcodes[3].x};
-        const uint32_t ab = __byte_perm(r[0][c4], r[1][c4], 0x5140);   // a0 b0 a1 b1
-        const uint32_t AB = __byte_perm(r[0][c4], r[1][c4], 0x7362);   // a2 b2 a3 b3
-        const uint32_t cd = __byte_perm(r[2][c4], r[3][c4], 0x5140);
-        const uint32_t CD = __byte_perm(r[2][c4], r[3][c4], 0x7362);
+        uint32_t r[4];   // four codes of each of the four rows
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          r[i] = c4 == 0 ? rcodes[i].x : c4 == 1 ? rcodes[i].y : c4 == 2 ? rcodes[i].z : rcodes[i].w;
+        const uint32_t ab = __byte_perm(r[0], r[1], 0x5140);   // a0 b0 a1 b1
+        const uint32_t AB = __byte_perm(r[0], r[1], 0x7362);   // a2 b2 a3 b3
+        const uint32_t cd = __byte_perm(r[2], r[3], 0x5140);
+        const uint32_t CD = __byte_perm(r[2], r[3], 0x7362);
         const int c = sub * 16 + 4 * c4;
         sh_codes[word_at(c, g)] = __byte_perm(ab, cd, 0x5410);
         sh_codes[word_at(c + 1, g)] = __byte_perm(ab, cd, 0x7632);

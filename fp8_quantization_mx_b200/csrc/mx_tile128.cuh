@@ -197,11 +197,12 @@ struct Vec {
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
   // 16-byte aligned p, all N elements present; read once (no L1 allocation). Not the
-  // read-only path: an output may be the input in place.
+  // read-only path: an output may be the input in place. (volatile, here and
+  // below: stays behind the wait for the kernel before)
   __device__ __forceinline__ void load(const typename E::T* p) {
 #pragma unroll
     for (int i = 0; i < kWords; i += 4)
-      asm("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
           : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
           : "l"(reinterpret_cast<const char*>(p) + 4 * i));
   }
@@ -214,13 +215,13 @@ struct Vec {
     uint32_t t[kWords + 4];
 #pragma unroll
     for (int i = 0; i < kWords; i += 4)
-      asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
           : "=r"(t[i]), "=r"(t[i + 1]), "=r"(t[i + 2]), "=r"(t[i + 3])
           : "l"(q + 4 * i));
 #pragma unroll
     for (int i = kWords; i < kWords + 4; ++i) t[i] = 0;
     if (off)
-      asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
           : "=r"(t[kWords]), "=r"(t[kWords + 1]), "=r"(t[kWords + 2]), "=r"(t[kWords + 3])
           : "l"(q + 4 * kWords));
 #pragma unroll
