@@ -486,14 +486,17 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
   }
 }
 
-// Any number of columns at any alignment, element tid + 256 j in thread tid: up
-// to 256 NJ columns in registers; beyond, a row is read twice and a thread adds
-// to its columns of the CTA's share of gw in memory. WARP: up to 32 NJ columns,
-// a warp per row.
+// Any number of columns at any alignment, element tid + nt j in thread tid: up
+// to nt NJ columns in registers (nt: 256 threads, 512 or 1024 for long rows);
+// beyond, a row is read twice and a thread adds to its columns of the CTA's
+// share of gw in memory. WARP: up to 32 NJ columns, a warp per row. With four
+// elements a thread the next row's loads are issued before this row's sums.
 template <int DT, int NJ, bool WARP>
-__global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(!WARP && NJ == 8 ? 1024 : 256, WARP && NJ > 8 ? 2 : !WARP && NJ == 8 ? 1 : 4)
+    norm_bwd_any_kernel(const NormBwdArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
+  constexpr bool kAhead = NJ == 4;
   __shared__ float red[2][64];
   dependent_launch();
   dependent_wait();
@@ -501,28 +504,41 @@ __global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(cons
   const int tid = rt.tid, nt = rt.nt;
   const T* w = static_cast<const T*>(a.weight);
   float* part = a.part + blockIdx.x * a.cols;
-  float gw[NJ], wv[NJ];
+  float gw[NJ], wv[NJ], g[NJ], h[NJ], o[NJ];
+  const auto load = [&](int64_t row, float(&gv)[NJ], float(&hv)[NJ], float(&ov)[NJ]) {
+    const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
+    const T* hh = static_cast<const T*>(a.h) + row * a.cols;
+    const T* gres = static_cast<const T*>(a.gres) + (a.gres ? row * a.cols : 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = tid + nt * j;
+      const bool in = c < a.cols && row < a.rows;
+      gv[j] = in ? E::to_float(gy[c]) : 0.0f;
+      hv[j] = in ? E::to_float(hh[c]) : 0.0f;
+      if (kAhead) ov[j] = in && a.gres ? E::to_float(gres[c]) : 0.0f;
+    }
+  };
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     gw[j] = 0.0f;
     wv[j] = tid + nt * j < a.cols ? E::to_float(w[tid + nt * j]) : 0.0f;
   }
+  if (kAhead) load(rt.first, g, h, o);
   int par = 0;
   for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
     const T* hh = static_cast<const T*>(a.h) + row * a.cols;
     const T* gres = a.gres ? static_cast<const T*>(a.gres) + row * a.cols : nullptr;
     T* gh = static_cast<T*>(a.gh) + row * a.cols;
-    float g[NJ], h[NJ], s[2] = {0.0f, 0.0f};
+    float gn[NJ], hn[NJ], on[NJ], s[2] = {0.0f, 0.0f};
+    if (kAhead) load(row + rt.step, gn, hn, on);
+    else load(row, g, h, o);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int64_t c = tid + nt * j;
-      g[j] = c < a.cols ? E::to_float(gy[c]) : 0.0f;
-      h[j] = c < a.cols ? E::to_float(hh[c]) : 0.0f;
       s[0] = fmaf(h[j], h[j], s[0]);
       s[1] = fmaf(g[j] * wv[j], h[j], s[1]);
     }
-    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += 256) {
+    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += nt) {
       const float v = E::to_float(hh[c]);
       s[0] = fmaf(v, v, s[0]);
       s[1] = fmaf(E::to_float(gy[c]) * E::to_float(w[c]), v, s[1]);
@@ -535,10 +551,17 @@ __global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(cons
       const int64_t c = tid + nt * j;
       const float n = h[j] * r;
       gw[j] = fmaf(g[j], n, gw[j]);
-      if (c < a.cols)
-        gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), gres ? E::to_float(gres[c]) : 0.0f));
+      if (c < a.cols) {
+        const float add = kAhead ? o[j] : gres ? E::to_float(gres[c]) : 0.0f;
+        gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), add));
+      }
+      if (kAhead) {
+        g[j] = gn[j];
+        h[j] = hn[j];
+        o[j] = on[j];
+      }
     }
-    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += 256) {
+    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += nt) {
       const float n = E::to_float(hh[c]) * r, v = E::to_float(gy[c]);
       part[c] = fmaf(v, n, row == blockIdx.x ? 0.0f : part[c]);
       gh[c] = E::from_float(
@@ -562,7 +585,7 @@ __global__ void __launch_bounds__(256, NJ <= 8 ? 4 : 2) norm_bwd_any_kernel(cons
   } else {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      if (tid + 256 * j < a.cols) part[tid + 256 * j] = gw[j];
+      if (tid + nt * j < a.cols) part[tid + nt * j] = gw[j];
   }
 }
 
@@ -651,12 +674,14 @@ cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
 template <int DT>
 cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaStream_t st) {
   const Shape s = shape_of(a.cols / 8, a.rows, sms);
-  // The kernels for any size: 256 threads; many rows of up to 512 columns a warp
-  // each (5324 x 355: 14.4 us, 18.1 with a CTA each; at 1001 columns its
-  // registers leave one CTA per SM and it takes 63 us for 27).
+  // The kernels for any size: many rows of up to 512 columns a warp each (5324 x
+  // 355: 14.4 us, 18.1 with a CTA each; at 1001 columns its registers leave one
+  // CTA per SM and it takes 63 us for 27); else a CTA each, of as many threads as
+  // keep the row in registers, four elements a thread where they are few.
   const bool warp = a.cols <= 512 && a.rows > 4 * sms;
-  const int nj = warp ? (a.cols <= 256 ? 8 : 16) : a.cols <= 1024 ? 4 : a.cols <= 2048 ? 8 : 16;
-  const int64_t any = (nj <= 8 ? 4 : 2) * sms;
+  const int nj = warp ? (a.cols <= 256 ? 8 : 16) : a.cols <= 1024 ? 4 : 8;
+  const int nt = warp || a.cols <= 2048 ? 256 : a.cols <= 4096 ? 512 : 1024;
+  const int64_t any = (nj <= 8 ? 1024 / nt : 2) * static_cast<int64_t>(sms);
   const int64_t any_rows = warp ? (a.rows + 7) / 8 : a.rows;
   int64_t grid = vec ? grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512)
                      : (any_rows < any ? any_rows : any);
@@ -664,10 +689,8 @@ cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaS
   cudaError_t e;
   if (!vec) {
     const auto kern = warp ? (nj == 8 ? norm_bwd_any_kernel<DT, 8, true> : norm_bwd_any_kernel<DT, 16, true>)
-                           : (nj == 4   ? norm_bwd_any_kernel<DT, 4, false>
-                              : nj == 8 ? norm_bwd_any_kernel<DT, 8, false>
-                                        : norm_bwd_any_kernel<DT, 16, false>);
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, 1, a);
+                           : (nj == 4 ? norm_bwd_any_kernel<DT, 4, false> : norm_bwd_any_kernel<DT, 8, false>);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(nt), 0, st, 1, a);
   } else {
     const auto kern = s.warp ? (s.nv == 1   ? norm_bwd_kernel<DT, 1, true>
                                 : s.nv == 2 ? norm_bwd_kernel<DT, 2, true>
