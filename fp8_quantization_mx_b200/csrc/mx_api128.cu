@@ -100,7 +100,7 @@ int mx_rms_norm_quant128(const void* x, int64_t ldx, const void* residual, const
 
 int64_t mx_rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
   if (check_matrix(rows, cols) != MX_OK) return -1;
-  return (rows < mxk::kNormParts ? rows : mxk::kNormParts) * cols * 4;
+  return (rows < mxk::kNormParts ? rows : mxk::kNormParts) * mxk::norm_part_pitch(cols) * 4;
 }
 
 int mx_rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const void* grad_residual,

@@ -60,8 +60,10 @@ cudaError_t launch_norm128(const void* x, int64_t ldx, const void* residual, con
                            int dtype, int64_t rows, int64_t cols, float eps, bool e5m2, bool pow2,
                            void* h, void* y, uint8_t* codes, int64_t ldc, float* scales,
                            int64_t lds, cudaStream_t st);
-// part: kNormParts * cols floats at most (min(rows, kNormParts) * cols).
+// part: min(rows, kNormParts) * norm_part_pitch(cols) floats (where rows start
+// at any element of a vector, so do their shares).
 constexpr int kNormParts = 592;
+constexpr int64_t norm_part_pitch(int64_t cols) { return cols % 8 ? (cols + 14) / 8 * 8 : cols; }
 cudaError_t launch_norm_bwd(const void* gy, const void* h, const void* weight, const void* gres,
                             int dtype, int64_t rows, int64_t cols, float eps, void* gh, float* gw,
                             float* part, cudaStream_t st);

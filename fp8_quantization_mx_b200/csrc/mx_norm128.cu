@@ -20,6 +20,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "mx_launch.h"
 #include "mx_pdl.cuh"
 #include "mx_tile128.cuh"
@@ -347,16 +349,74 @@ struct NormBwdArgs {
   const void* weight;     // [cols]
   const void* gres;       // [rows, cols] or null
   void* gh;               // [rows, cols]
-  float* part;            // [gridDim.x, cols]: each CTA's share of gw
+  float* part;            // [gridDim.x, pitch]: each CTA's share of gw
+  int64_t pitch;
   int64_t rows, cols;
   float eps;
 };
+
+// The first n elements of the aligned vector at p (any n), the rest 0: by
+// predicated words, so that no branch waits for its data.
+template <int DT>
+__device__ __forceinline__ void load_head(Vec<DT, 8>& v, const typename Elem<DT>::T* p, int n) {
+#pragma unroll
+  for (int k = 0; k < v.kWords; ++k) {
+    const char* q = reinterpret_cast<const char*>(p) + 4 * k;
+    if constexpr (DT == kFP32)
+      asm volatile("{.reg .pred f; setp.gt.s32 f, %2, 0; mov.b32 %0, 0; @f ld.global.b32 %0, [%1];}"
+                   : "=&r"(v.w[k]) : "l"(q), "r"(n - k));
+    else
+      asm volatile("{.reg .pred f, h; setp.gt.s32 f, %2, 1; setp.eq.s32 h, %2, 1; mov.b32 %0, 0;\n"
+                   "@f ld.global.b32 %0, [%1]; @h ld.global.u16 %0, [%1];}"
+                   : "=&r"(v.w[k]) : "l"(q), "r"(n - 2 * k));
+  }
+}
+
+// Elements off..off + 7 (off 1 to 8) of the two vectors a, b.
+template <int DT>
+__device__ __forceinline__ Vec<DT, 8> between(const Vec<DT, 8>& a, const Vec<DT, 8>& b, int off) {
+  constexpr int W = Vec<DT, 8>::kWords;
+  uint32_t t[2 * W + 1];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    t[i] = a.w[i];
+    t[W + i] = b.w[i];
+  }
+  t[2 * W] = 0;
+#pragma unroll
+  for (int e = 8; e * W >= 8; e /= 2)   // elements that are whole words
+#pragma unroll
+    for (int i = 0; i + e * W / 8 <= 2 * W; ++i) t[i] = off & e ? t[i + e * W / 8] : t[i];
+  Vec<DT, 8> v;
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    v.w[i] = DT == kFP32 ? t[i] : __funnelshift_r(t[i], t[i + 1], (off & 1) * 16);
+  return v;
+}
+
+// Stores elements lo..hi - 1 of a vector.
+template <int DT>
+__device__ __forceinline__ void store_part(typename Elem<DT>::T* p, Vec<DT, 8> v, int lo, int hi) {
+  using U = typename std::conditional<DT == kFP32, uint32_t, uint16_t>::type;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i >= lo && i < hi)
+      reinterpret_cast<U*>(p)[i] = DT == kFP32 ? v.w[i % v.kWords] : v.w[i / 2] >> (16 * (i & 1));
+}
 
 // A thread keeps its columns' share of gw in registers (shared memory with four
 // vectors a thread in a CTA) over all its rows; WARP: the CTA's eight warps add
 // theirs up at the end. (With four vectors a thread the next row's loads do not
 // fit the registers and wait.)
-template <int DT, int NV, bool WARP>
+//
+// ODD: the columns are no multiple of 8, so that rows start at any element of a
+// vector. The vectors are those of the memory then, shifted by the row's start
+// among them; the first and the last of a row hold elements of its neighbours,
+// which are masked. A thread takes rows a multiple of 8 apart (the launch sees
+// to that), whose shifts are the same, and so keeps its columns. (4097 x 3001:
+// 25.9 us, 85 with an element at a time; 4 x 6940 5.6 us for 7.7; 5324 x 355 11.2
+// for 14.1. Loads that a branch had to wait for cost 0.7 us each.)
+template <int DT, int NV, bool WARP, bool ODD>
 __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WARP && NV == 2 ? 2 : 1)
     norm_bwd_kernel(const NormBwdArgs a) {
   using T = typename Elem<DT>::T;
@@ -368,7 +428,25 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
   const int tid = rt.tid, nt = rt.nt;
   dependent_launch();
   dependent_wait();
-  const int nvec = static_cast<int>(a.cols / 8);
+  const int cols = static_cast<int>(a.cols);
+  const int shift = ODD ? static_cast<int>(rt.first * a.cols & 7) : 0;
+  const int nvec = ODD ? (shift + cols + 7) / 8 : cols / 8;
+  // the row's elements of vector i: lo..hi - 1 (ODD)
+  const auto lo_of = [&](int i) { return i == 0 ? shift : 0; };
+  const auto hi_of = [&](int i) { return min(8, shift + cols - 8 * i); };
+  const auto whole = [&](int i) { return !ODD || (lo_of(i) == 0 && hi_of(i) == 8); };
+  const auto at_of = [&](int64_t row, int i) {   // a multiple of 8, at least 0
+    return row * a.cols - shift + 8 * i;
+  };
+  const auto read = [&](Vec<DT, 8>& v, const void* p, int64_t row, int i) {
+    const T* q = static_cast<const T*>(p) + at_of(row, i);
+    if (ODD && i == nvec - 1 && row == a.rows - 1) load_head(v, q, hi_of(i));   // the tensor's end
+    else v.load(q);
+  };
+  // The elements of other rows, as 0: once they are there, so that no load waits.
+  const auto mask = [&](Vec<DT, 8>& v, int i) {
+    if (!whole(i)) v.keep(lo_of(i), hi_of(i));
+  };
   float gw[kShared ? 1 : NV][8];
   Vec<DT, 8> wv[NV], gv[NV], hv[NV];
   const auto load = [&](int64_t row, Vec<DT, 8>(&g)[NV], Vec<DT, 8>(&h)[NV]) {
@@ -378,16 +456,31 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
       g[j].zero();
       h[j].zero();
       if (i < nvec && row < a.rows) {
-        g[j].load(static_cast<const T*>(a.gy) + row * a.cols + 8 * i);
-        h[j].load(static_cast<const T*>(a.h) + row * a.cols + 8 * i);
+        read(g[j], a.gy, row, i);
+        read(h[j], a.h, row, i);
       }
     }
   };
+  if (kAhead) load(rt.first, gv, hv);
+  Vec<DT, 8> wn[ODD ? NV : 1];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = tid + j * nt;
+    const T* p = static_cast<const T*>(a.weight) + 8 * i;
     wv[j].zero();
-    if (i < nvec) wv[j].load(static_cast<const T*>(a.weight) + 8 * i);
+    if constexpr (ODD) wn[j].zero();
+    if (i < nvec) {
+      if constexpr (ODD) {
+        if (i > 0) {
+          if (8 * i <= cols) wv[j].load(p - 8);
+          else load_head(wv[j], p - 8, cols - 8 * i + 8);
+        }
+        if (8 * i + 8 <= cols) wn[j].load(p);
+        else load_head(wn[j], p, cols - 8 * i);
+      } else {
+        wv[j].load(p);
+      }
+    }
     if constexpr (kShared) {
       sh_gw[(2 * j) * nt + tid] = sh_gw[(2 * j + 1) * nt + tid] = make_float4(0, 0, 0, 0);
     } else {
@@ -395,7 +488,9 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
       for (int e = 0; e < 8; ++e) gw[j][e] = 0.0f;
     }
   }
-  if (kAhead) load(rt.first, gv, hv);
+  if constexpr (ODD)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) wv[j] = between<DT>(wv[j], wn[j], 8 - shift);
   int par = 0;
   for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     Vec<DT, 8> gn[NV], hn[NV], rv[NV];
@@ -405,7 +500,14 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * nt;
       rv[j].zero();
-      if (a.gres && i < nvec) rv[j].load(static_cast<const T*>(a.gres) + row * a.cols + 8 * i);
+      if (a.gres && i < nvec) read(rv[j], a.gres, row, i);
+    }
+    if constexpr (ODD) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        mask(gv[j], tid + j * nt);
+        mask(hv[j], tid + j * nt);
+      }
     }
     float s[2] = {0.0f, 0.0f};   // sum h^2, sum gy w h
 #pragma unroll
@@ -440,10 +542,12 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
         sh_gw[(2 * j + 1) * nt + tid] = make_float4(w[4], w[5], w[6], w[7]);
       }
       if (i < nvec) {
+        T* out = static_cast<T*>(a.gh) + at_of(row, i);
         Vec<DT, 8> ov;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ov.set2(e, o[2 * e], o[2 * e + 1]);
-        ov.store(static_cast<T*>(a.gh) + row * a.cols + 8 * i);
+        if (whole(i)) ov.store(out);
+        else store_part<DT>(out, ov, lo_of(i), hi_of(i));
       }
       if (kAhead) {
         gv[j] = gn[j];
@@ -451,29 +555,37 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
       }
     }
   }
-  float* part = a.part + blockIdx.x * a.cols;
+  float* part = a.part + blockIdx.x * a.pitch;
   if constexpr (WARP) {
-    // the warps' shares, vector by vector: [8 warps][32 lanes][8]
-    __shared__ __align__(16) float sh_part[8][32 * 8];
+    // the warps' shares (warp w's shifted by its rows'); ODD: all at once, else
+    // vector by vector: [8 warps][32 lanes][8]
+    constexpr int kAtOnce = ODD ? NV : 1;
+    __shared__ __align__(16) float sh_part[8][kAtOnce * 256 + (ODD ? 8 : 0)];
     const int warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (j) __syncthreads();
+    for (int j0 = 0; j0 < NV; j0 += kAtOnce) {
+      if (j0) __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sh_part[warp][tid * 8 + e] = gw[j][e];
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sh_part[warp][j * 256 + tid * 8 + e] = gw[j0 + j][e];
       __syncthreads();
-      float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) sum += sh_part[w][threadIdx.x];
-      const int c = j * 256 + threadIdx.x;
-      if (c < a.cols) part[c] = sum;
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int at = j * 256 + threadIdx.x, c = j0 * 256 + at;
+        if (c >= cols) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += sh_part[w][at + (ODD ? w * cols & 7 : 0)];
+        part[c] = sum;
+      }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * nt;
       if (i < nvec) {
-        float4* p = reinterpret_cast<float4*>(part + 8 * i);
+        float4* p = reinterpret_cast<float4*>(part + 8 * i);   // (ODD: shifted as the row is)
         if constexpr (kShared) {
           p[0] = sh_gw[(2 * j) * nt + tid];
           p[1] = sh_gw[(2 * j + 1) * nt + tid];
@@ -487,58 +599,46 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
 }
 
 // Any number of columns at any alignment, element tid + nt j in thread tid: up
-// to nt NJ columns in registers (nt: 256 threads, 512 or 1024 for long rows);
+// to 8 nt columns in registers (nt: 256 threads, 512 or 1024 for long rows);
 // beyond, a row is read twice and a thread adds to its columns of the CTA's
-// share of gw in memory. WARP: up to 32 NJ columns, a warp per row. With four
-// elements a thread the next row's loads are issued before this row's sums.
-template <int DT, int NJ, bool WARP>
-__global__ void __launch_bounds__(!WARP && NJ == 8 ? 1024 : 256, WARP && NJ > 8 ? 2 : !WARP && NJ == 8 ? 1 : 4)
-    norm_bwd_any_kernel(const NormBwdArgs a) {
+// share of gw in memory.
+template <int DT>
+__global__ void __launch_bounds__(1024, 1) norm_bwd_any_kernel(const NormBwdArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr bool kAhead = NJ == 4;
+  constexpr int NJ = 8;
   __shared__ float red[2][64];
   dependent_launch();
   dependent_wait();
-  const RowThreads<WARP> rt;
+  const RowThreads<false> rt;
   const int tid = rt.tid, nt = rt.nt;
   const T* w = static_cast<const T*>(a.weight);
-  float* part = a.part + blockIdx.x * a.cols;
-  float gw[NJ], wv[NJ], g[NJ], h[NJ], o[NJ];
-  const auto load = [&](int64_t row, float(&gv)[NJ], float(&hv)[NJ], float(&ov)[NJ]) {
-    const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
-    const T* hh = static_cast<const T*>(a.h) + row * a.cols;
-    const T* gres = static_cast<const T*>(a.gres) + (a.gres ? row * a.cols : 0);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t c = tid + nt * j;
-      const bool in = c < a.cols && row < a.rows;
-      gv[j] = in ? E::to_float(gy[c]) : 0.0f;
-      hv[j] = in ? E::to_float(hh[c]) : 0.0f;
-      if (kAhead) ov[j] = in && a.gres ? E::to_float(gres[c]) : 0.0f;
-    }
-  };
+  float* part = a.part + blockIdx.x * a.pitch;
+  float gw[NJ], wv[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     gw[j] = 0.0f;
     wv[j] = tid + nt * j < a.cols ? E::to_float(w[tid + nt * j]) : 0.0f;
   }
-  if (kAhead) load(rt.first, g, h, o);
   int par = 0;
   for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     const T* gy = static_cast<const T*>(a.gy) + row * a.cols;
     const T* hh = static_cast<const T*>(a.h) + row * a.cols;
     const T* gres = a.gres ? static_cast<const T*>(a.gres) + row * a.cols : nullptr;
     T* gh = static_cast<T*>(a.gh) + row * a.cols;
-    float gn[NJ], hn[NJ], on[NJ], s[2] = {0.0f, 0.0f};
-    if (kAhead) load(row + rt.step, gn, hn, on);
-    else load(row, g, h, o);
+    float g[NJ], h[NJ], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = tid + nt * j;
+      g[j] = c < a.cols ? E::to_float(gy[c]) : 0.0f;
+      h[j] = c < a.cols ? E::to_float(hh[c]) : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       s[0] = fmaf(h[j], h[j], s[0]);
       s[1] = fmaf(g[j] * wv[j], h[j], s[1]);
     }
-    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += nt) {
+    for (int64_t c = tid + nt * NJ; c < a.cols; c += nt) {
       const float v = E::to_float(hh[c]);
       s[0] = fmaf(v, v, s[0]);
       s[1] = fmaf(E::to_float(gy[c]) * E::to_float(w[c]), v, s[1]);
@@ -551,49 +651,27 @@ __global__ void __launch_bounds__(!WARP && NJ == 8 ? 1024 : 256, WARP && NJ > 8 
       const int64_t c = tid + nt * j;
       const float n = h[j] * r;
       gw[j] = fmaf(g[j], n, gw[j]);
-      if (c < a.cols) {
-        const float add = kAhead ? o[j] : gres ? E::to_float(gres[c]) : 0.0f;
-        gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), add));
-      }
-      if (kAhead) {
-        g[j] = gn[j];
-        h[j] = hn[j];
-        o[j] = on[j];
-      }
+      if (c < a.cols)
+        gh[c] = E::from_float(fmaf(r, fmaf(-n, m, g[j] * wv[j]), gres ? E::to_float(gres[c]) : 0.0f));
     }
-    for (int64_t c = tid + nt * NJ; !WARP && c < a.cols; c += nt) {
+    for (int64_t c = tid + nt * NJ; c < a.cols; c += nt) {
       const float n = E::to_float(hh[c]) * r, v = E::to_float(gy[c]);
       part[c] = fmaf(v, n, row == blockIdx.x ? 0.0f : part[c]);
       gh[c] = E::from_float(
           fmaf(r, fmaf(-n, m, v * E::to_float(w[c])), gres ? E::to_float(gres[c]) : 0.0f));
     }
   }
-  if constexpr (WARP) {
-    __shared__ float sh_part[8][32];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      if (j) __syncthreads();
-      sh_part[threadIdx.x >> 5][tid] = gw[j];
-      __syncthreads();
-      if (threadIdx.x < 32 && tid + 32 * j < a.cols) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int v = 0; v < 8; ++v) sum += sh_part[v][tid];
-        part[tid + 32 * j] = sum;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (tid + nt * j < a.cols) part[tid + nt * j] = gw[j];
-  }
+  for (int j = 0; j < NJ; ++j)
+    if (tid + nt * j < a.cols) part[tid + nt * j] = gw[j];
 }
 
 // gw[c] = sum of the CTAs' shares, in an order that depends on their number
 // alone: 32 warps take every 32nd share of 32 columns, then add up. (Latency:
 // with 8 warps the sum of 444 shares took 4 us.)
-__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int nparts,
-                                                            int64_t cols, float* gw) {
+// `shifted`: share p starts at element p cols mod 8.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int nparts, int64_t pitch,
+                                                            int64_t cols, bool shifted, float* gw) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   dependent_launch();
@@ -602,7 +680,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, i
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = warp; p < nparts; p += 32) s += part[p * cols + c];
+    for (int p = warp; p < nparts; p += 32)
+      s += part[p * pitch + c + (shifted ? p * static_cast<int>(cols) & 7 : 0)];
   }
   red[warp][lane] = s;
   __syncthreads();
@@ -617,8 +696,9 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 // How a row of nvec vectors is spread: up to 1024 elements one warp (one, two
 // or four vectors a lane), up to 8192 a CTA with two vectors a thread, up to
 // 16384 four (512 threads at most); beyond, the kernel for any size. A few rows
-// of up to 2048 elements take one vector a thread: what counts is one row's
-// time (1 x 2048: 1.8 us, 2.06 with two; 16387 x 2048: 44.3 us, 40.5 with two).
+// of 256 to 2048 elements take a CTA each with one vector a thread: what counts
+// is one row's time (forward 1 x 2048: 1.8 us, 2.06 with two vectors, but 16387 x
+// 2048 44.3 us, 40.5 with two; gradient 1 x 1000: 2.7 us, 3.45 with one warp).
 constexpr int64_t kMaxVecCols = 16384;
 struct Shape {
   bool warp;
@@ -626,8 +706,9 @@ struct Shape {
   unsigned nt;
 };
 Shape shape_of(int64_t nvec, int64_t rows, int sms) {
-  if (nvec <= 128) return {true, nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 256};
-  const int nv = nvec <= 256 && rows <= 4 * sms ? 1 : nvec <= 1024 ? 2 : 4;
+  const bool few = rows <= 4 * sms;
+  if (nvec <= 32 || (nvec <= 128 && !few)) return {true, nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 256};
+  const int nv = nvec <= 256 && few ? 1 : nvec <= 1024 ? 2 : 4;
   return {false, nv, static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)};
 }
 
@@ -671,44 +752,46 @@ cudaError_t launch_norm(const NormArgs& a, bool vec, int sms, cudaStream_t st) {
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), 0, st, 1, a);
 }
 
+template <int DT, bool ODD>
+cudaError_t launch_bwd_vec(const NormBwdArgs& a, const Shape& s, int64_t grid, cudaStream_t st) {
+  const auto kern = s.warp ? (s.nv == 1   ? norm_bwd_kernel<DT, 1, true, ODD>
+                              : s.nv == 2 ? norm_bwd_kernel<DT, 2, true, ODD>
+                                          : norm_bwd_kernel<DT, 4, true, ODD>)
+                           : (s.nv == 1   ? norm_bwd_kernel<DT, 1, false, ODD>
+                              : s.nv == 2 ? norm_bwd_kernel<DT, 2, false, ODD>
+                                          : norm_bwd_kernel<DT, 4, false, ODD>);
+  const size_t smem = !s.warp && s.nv == 4 ? s.nt * size_t(4 * 8 * 4) : 0;   // up to 64 KiB
+  if (smem) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 8 * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), smem, st, 1, a);
+}
+
 template <int DT>
 cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaStream_t st) {
-  const Shape s = shape_of(a.cols / 8, a.rows, sms);
-  // The kernels for any size: many rows of up to 512 columns a warp each (5324 x
-  // 355: 14.4 us, 18.1 with a CTA each; at 1001 columns its registers leave one
-  // CTA per SM and it takes 63 us for 27); else a CTA each, of as many threads as
-  // keep the row in registers, four elements a thread where they are few.
-  const bool warp = a.cols <= 512 && a.rows > 4 * sms;
-  const int nj = warp ? (a.cols <= 256 ? 8 : 16) : a.cols <= 1024 ? 4 : 8;
-  const int nt = warp || a.cols <= 2048 ? 256 : a.cols <= 4096 ? 512 : 1024;
-  const int64_t any = (nj <= 8 ? 1024 / nt : 2) * static_cast<int64_t>(sms);
-  const int64_t any_rows = warp ? (a.rows + 7) / 8 : a.rows;
-  int64_t grid = vec ? grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512)
-                     : (any_rows < any ? any_rows : any);
-  if (grid > kNormParts) grid = kNormParts;
+  const bool odd = a.cols % 8 != 0;
+  const Shape s = shape_of(odd ? (a.cols + 14) / 8 : a.cols / 8, a.rows, sms);
+  int64_t grid;
   cudaError_t e;
-  if (!vec) {
-    const auto kern = warp ? (nj == 8 ? norm_bwd_any_kernel<DT, 8, true> : norm_bwd_any_kernel<DT, 16, true>)
-                           : (nj == 4 ? norm_bwd_any_kernel<DT, 4, false> : norm_bwd_any_kernel<DT, 8, false>);
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(nt), 0, st, 1, a);
+  if (vec) {
+    grid = grid_for(s, a.rows, sms, s.nv == 1 ? 768 : s.nv == 4 && s.warp ? 256 : 512);
+    if (grid > kNormParts) grid = kNormParts;
+    // rows a multiple of 8 apart to a CTA (a warp's are)
+    if (odd && !s.warp && grid < a.rows) grid = grid / 8 * 8;
+    e = odd ? launch_bwd_vec<DT, true>(a, s, grid, st) : launch_bwd_vec<DT, false>(a, s, grid, st);
   } else {
-    const auto kern = s.warp ? (s.nv == 1   ? norm_bwd_kernel<DT, 1, true>
-                                : s.nv == 2 ? norm_bwd_kernel<DT, 2, true>
-                                            : norm_bwd_kernel<DT, 4, true>)
-                             : (s.nv == 1   ? norm_bwd_kernel<DT, 1, false>
-                                : s.nv == 2 ? norm_bwd_kernel<DT, 2, false>
-                                            : norm_bwd_kernel<DT, 4, false>);
-    const size_t smem = !s.warp && s.nv == 4 ? s.nt * size_t(4 * 8 * 4) : 0;   // up to 64 KiB
-    if (smem) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 8 * 4);
-      if (e != cudaSuccess) return e;
-    }
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(s.nt), smem, st, 1, a);
+    const int nt = a.cols <= 2048 ? 256 : a.cols <= 4096 ? 512 : 1024;
+    const int64_t most = static_cast<int64_t>(1024 / nt) * sms;
+    grid = a.rows < most ? a.rows : most;
+    if (grid > kNormParts) grid = kNormParts;
+    e = launch_dependent(norm_bwd_any_kernel<DT>, dim3(static_cast<unsigned>(grid)), dim3(nt), 0, st, 1, a);
   }
   if (e != cudaSuccess) return e;
   return launch_dependent(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)),
-                          dim3(1024), 0, st, 1, static_cast<const float*>(a.part),
-                          static_cast<int>(grid), a.cols, gw);
+                          dim3(1024), 0, st, 1, static_cast<const float*>(a.part), static_cast<int>(grid),
+                          a.pitch, a.cols, vec && odd && !s.warp, gw);
 }
 
 cudaError_t device_sms(int* sms) {
@@ -765,10 +848,12 @@ cudaError_t launch_norm_bwd(const void* gy, const void* h, const void* weight, c
   a.gres = gres;
   a.gh = gh;
   a.part = part;
+  a.pitch = norm_part_pitch(cols);
   a.rows = rows;
   a.cols = cols;
   a.eps = eps;
-  const bool vec = cols % 8 == 0 && cols <= kMaxVecCols && aligned16(gy) && aligned16(h) &&
+  const bool odd = cols % 8 != 0;
+  const bool vec = cols <= kMaxVecCols - (odd ? 14 : 0) && aligned16(gy) && aligned16(h) &&
                    aligned16(weight) && aligned16(gres) && aligned16(gh) && aligned16(part);
   int sms = 0;
   const cudaError_t e = device_sms(&sms);

@@ -231,6 +231,15 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(t[i], t[i + 1], (off & 3) * 8);
   }
+  // Elements other than lo..hi - 1 become 0.
+  __device__ __forceinline__ void keep(int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < lo || i >= hi) {
+        if constexpr (DT == kFP32) w[i] = 0;
+        else w[i / 2] &= (i & 1) ? 0xffffu : 0xffff0000u;
+      }
+  }
   // The first n elements, one at a time; the rest 0.
   __device__ __forceinline__ void load_some(const typename E::T* p, int64_t n) {
     zero();

@@ -207,7 +207,32 @@ def test_norm_nan_stays_in_its_row(mx, cuda):
         assert torch.equal(codes[i], clean[0][i]) and torch.equal(scales[i], clean[1][i])
 
 
-@pytest.mark.parametrize("shape", NORM_SHAPES + [(1500, 64), (333, 2048)], ids=str)
+# no multiples of 8: every spread of a row over threads, more rows than CTAs
+ODD_SHAPES = [(9, 3), (5000, 7), (4801, 241), (5324, 355), (3000, 1001), (2600, 1017), (1, 1019),
+              (460, 1027), (600, 1019), (1100, 1030), (900, 3001), (450, 7004), (300, 9001),
+              (200, 16369), (170, 16371), (50, 4099)]
+
+
+def check_gradient(mx, g, h, w, gr):
+    (rows, cols), t = h.shape, h.dtype
+    gh, gw = mx.rms_norm_bwd(g, h, w, eps=1e-5, grad_residual=gr)
+    eps = float(np.float32(1e-5))
+    want, want_w = P.norm_bwd(f64(g), f64(h), f64(w), eps, None if gr is None else f64(gr))
+    # each term of the sum, by its magnitude: n / 2 + 8 roundings of r, the
+    # mean's n more
+    h64, gw64 = f64(h), f64(g) * f64(w)
+    r = 1 / np.sqrt((h64 * h64).mean(1, keepdims=True) + eps)
+    n = np.abs(h64 * r)
+    mag = r * (np.abs(gw64) + n * (np.abs(gw64) * n).mean(1, keepdims=True))
+    err = (2 * cols + 16) * U32 * mag
+    tiny = torch.finfo(t).tiny if t != torch.float16 else 2.0 ** -25
+    assert np.all(np.abs(f64(gh) - want) <= half_step(t) * np.abs(want) + (1 + 2 ** -8) * err + tiny)
+    mag_w = (np.abs(f64(g)) * n).sum(0)
+    assert np.all(np.abs(f64(gw) - want_w) <= (cols / 2 + rows + 16) * U32 * mag_w)
+    return gh, gw
+
+
+@pytest.mark.parametrize("shape", NORM_SHAPES + [(1500, 64), (333, 2048)] + ODD_SHAPES, ids=str)
 def test_norm_gradient_equals_the_formula(mx, cuda, shape):
     rows, cols = shape
     for i, (dt, res) in enumerate([("bf16", True), ("fp16", False), ("fp32", True)]):
@@ -215,26 +240,39 @@ def test_norm_gradient_equals_the_formula(mx, cuda, shape):
         h, g = values(rows, cols, t, 27 + i), values(rows, cols, t, 37 + i)
         gr = values(rows, cols, t, 47 + i) if res else None
         w = (1 + 0.2 * torch.randn(cols, generator=torch.Generator().manual_seed(i))).to(t).cuda()
-        gh, gw = mx.rms_norm_bwd(g, h, w, eps=1e-5, grad_residual=gr)
-        eps = float(np.float32(1e-5))
-        want, want_w = P.norm_bwd(f64(g), f64(h), f64(w), eps, None if gr is None else f64(gr))
-        # each term of the sum, by its magnitude: n / 2 + 8 roundings of r, the
-        # mean's n more
-        h64, gw64 = f64(h), f64(g) * f64(w)
-        r = 1 / np.sqrt((h64 * h64).mean(1, keepdims=True) + eps)
-        n = np.abs(h64 * r)
-        mag = r * (np.abs(gw64) + n * (np.abs(gw64) * n).mean(1, keepdims=True))
-        err = (2 * cols + 16) * U32 * mag
-        tiny = torch.finfo(t).tiny if t != torch.float16 else 2.0 ** -25
-        assert np.all(np.abs(f64(gh) - want) <= half_step(t) * np.abs(want) + (1 + 2 ** -8) * err + tiny)
-        mag_w = (np.abs(f64(g)) * n).sum(0)
-        assert np.all(np.abs(f64(gw) - want_w) <= (cols / 2 + rows + 16) * U32 * mag_w)
+        gh, gw = check_gradient(mx, g, h, w, gr)
         # the same call gives the same bits, and works in place
         again = mx.rms_norm_bwd(g, h, w, eps=1e-5, grad_residual=gr)
         assert torch.equal(again[0], gh) and torch.equal(again[1], gw)
         held = g.clone()
         got = mx.rms_norm_bwd(held, h, w, eps=1e-5, grad_residual=gr, out=held)
         assert torch.equal(got[0], gh) and torch.equal(got[1], gw)
+
+
+@pytest.mark.parametrize("shape", [(70, 131), (33, 3000), (700, 5001), (3, 16392)], ids=str)
+def test_norm_gradient_of_unaligned_tensors(mx, cuda, shape):
+    """Tensors that start at any element, each at another."""
+    rows, cols = shape
+    for t in (torch.bfloat16, torch.float32):
+        g, h, gr = (torch.empty(rows * cols + 8, dtype=t, device=cuda)[i:i + rows * cols].view(rows, cols)
+                    .copy_(values(rows, cols, t, 57 + i)) for i in (1, 2, 3))
+        w = torch.ones(cols + 1, dtype=t, device=cuda)[1:]
+        check_gradient(mx, g, h, w, gr)
+        check_gradient(mx, values(rows, cols, t, 61), values(rows, cols, t, 62), w, None)
+
+
+@pytest.mark.parametrize("cols", [3, 131, 355, 1001, 2003, 9001])
+def test_norm_gradient_nan_stays_in_its_row(mx, cuda, cols):
+    """Rows that share 16 bytes with one that holds NaN or Inf."""
+    for t in (torch.bfloat16, torch.float32):
+        g, h, gr = (values(20, cols, t, 67 + i) for i in range(3))
+        w = torch.ones(cols, dtype=t, device=cuda)
+        clean = mx.rms_norm_bwd(g, h, w, grad_residual=gr)[0]
+        for x in (g, h, gr):
+            x[3], x[10] = float("nan"), float("inf")
+        got = mx.rms_norm_bwd(g, h, w, grad_residual=gr)[0]
+        rest = [i for i in range(20) if i not in (3, 10)]
+        assert torch.isnan(got[[3, 10]]).all() and torch.equal(got[rest], clean[rest])
 
 
 # ---------------------------------------------------------------- the GEMM --
