@@ -15,8 +15,8 @@
 // B200 with a copy bandwidth of 6.45 TB/s, bf16 with the residual: forward
 // 16387 x 4096 76.9 us (95% of the bytes' time), 8192 x 8192 85 us (86%), 65536
 // x 512 41.7 us (88%), one row of 2048 1.8 us; gradient 16384 x 4096 91.5 us
-// (91%), 65536 x 512 47.2 us (88%), 1999 x 2048 10.6 us (36%: four and a half
-// rows per CTA, then the second kernel's sum of 444 shares of gw).
+// (91%), 65536 x 512 47.2 us (88%), 1999 x 2048 9.5 us (40%: three or four
+// rows per CTA, then the second kernel's sum of 592 shares of gw).
 
 #include <cuda_runtime.h>
 
@@ -667,27 +667,35 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd_any_kernel(const NormBwdArgs
 }
 
 // gw[c] = sum of the CTAs' shares, in an order that depends on their number
-// alone: 32 warps take every 32nd share of 32 columns, then add up. (Latency:
-// with 8 warps the sum of 444 shares took 4 us.)
+// alone: C threads side by side take C columns of every (1024 / C)th share, then
+// a warp adds up each column. Bound by latency: C is the smallest (8, 16 or 32)
+// that gives no SM a second CTA (1999 x 2048, 592 shares: 16 columns 9.5 us with
+// the first kernel, 32 10.6; 700 x 8192: 16 columns 13.8 us, 32 12.4).
 // `shifted`: share p starts at element p cols mod 8.
+template <int C>
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int nparts, int64_t pitch,
                                                             int64_t cols, bool shifted, float* gw) {
-  __shared__ float red[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kGroups = 1024 / C;
+  __shared__ float red[C][kGroups + 1];
+  const int col = threadIdx.x % C, group = threadIdx.x / C;
   dependent_launch();
   dependent_wait();
-  const int64_t c = blockIdx.x * int64_t(32) + lane;
+  const int64_t c = blockIdx.x * int64_t(C) + col;
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = warp; p < nparts; p += 32)
+    for (int p = group; p < nparts; p += kGroups)
       s += part[p * pitch + c + (shifted ? p * static_cast<int>(cols) & 7 : 0)];
   }
-  red[warp][lane] = s;
+  red[col][group] = s;
   __syncthreads();
-  // warp w adds up column w
-  s = warp_sum(red[lane][warp]);
-  const int64_t o = blockIdx.x * int64_t(32) + warp;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= C) return;
+  s = red[warp][lane];
+#pragma unroll
+  for (int i = 32; i < kGroups; i += 32) s += red[warp][lane + i];
+  s = warp_sum(s);
+  const int64_t o = blockIdx.x * int64_t(C) + warp;
   if (lane == 0 && o < cols) gw[o] = s;
 }
 
@@ -789,9 +797,11 @@ cudaError_t launch_bwd(const NormBwdArgs& a, bool vec, int sms, float* gw, cudaS
     e = launch_dependent(norm_bwd_any_kernel<DT>, dim3(static_cast<unsigned>(grid)), dim3(nt), 0, st, 1, a);
   }
   if (e != cudaSuccess) return e;
-  return launch_dependent(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)),
-                          dim3(1024), 0, st, 1, static_cast<const float*>(a.part), static_cast<int>(grid),
-                          a.pitch, a.cols, vec && odd && !s.warp, gw);
+  const int c = a.cols <= 8 * sms ? 8 : a.cols <= 16 * sms ? 16 : 32;
+  const auto kern = c == 8 ? norm_bwd_sum_kernel<8> : c == 16 ? norm_bwd_sum_kernel<16> : norm_bwd_sum_kernel<32>;
+  return launch_dependent(kern, dim3(static_cast<unsigned>((a.cols + c - 1) / c)), dim3(1024), 0, st, 1,
+                          static_cast<const float*>(a.part), static_cast<int>(grid), a.pitch, a.cols,
+                          vec && odd && !s.warp, gw);
 }
 
 cudaError_t device_sms(int* sms) {
