@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libmx.so")
 SOURCES = ["mx_api.cu", "mx_kernels.cu", "mx_bat.cu", "mx_gemm.cu", "mx_api128.cu", "mx_quant128.cu",
            "mx_norm128.cu", "mx_gemm128.cu"]
 HEADERS = ["mx_device.cuh", "mx_launch.h", "mx_stream.cuh", "mx_tc.cuh", "mx_tile128.cuh",
-           "mx_gemm128.h", "mx_pdl.cuh"]
+           "mx_gemm128.h", "mx_pdl.cuh", "mx_rowvec.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
               "-fmad=true", "-Xcompiler", "-fPIC,-O2", "-cudart", "static"]

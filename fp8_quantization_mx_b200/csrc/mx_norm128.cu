@@ -24,6 +24,7 @@
 
 #include "mx_launch.h"
 #include "mx_pdl.cuh"
+#include "mx_rowvec.h"
 #include "mx_tile128.cuh"
 
 namespace mxk {
@@ -410,12 +411,13 @@ __device__ __forceinline__ void store_part(typename Elem<DT>::T* p, Vec<DT, 8> v
 // fit the registers and wait.)
 //
 // ODD: the columns are no multiple of 8, so that rows start at any element of a
-// vector. The vectors are those of the memory then, shifted by the row's start
-// among them; the first and the last of a row hold elements of its neighbours,
-// which are masked. A thread takes rows a multiple of 8 apart (the launch sees
-// to that), whose shifts are the same, and so keeps its columns. (4097 x 3001:
-// 25.9 us, 85 with an element at a time; 4 x 6940 5.6 us for 7.7; 5324 x 355 11.2
-// for 14.1. Loads that a branch had to wait for cost 0.7 us each.)
+// vector of the memory (mx_rowvec.h). A row's first and last vector hold elements
+// of its neighbours, which are masked: in place, another CTA may be writing those
+// meanwhile. Reads stop at the matrix's end. A thread takes rows a multiple of 8
+// apart (the launch sees to that), whose shifts are the same, and so keeps its
+// columns. (4097 x 3001: 25.9 us, 85 with an element at a time; 4 x 6940 5.6 us
+// for 7.7; 5324 x 355 11.2 for 14.1. Loads that a branch had to wait for cost
+// 0.7 us each.)
 template <int DT, int NV, bool WARP, bool ODD>
 __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WARP && NV == 2 ? 2 : 1)
     norm_bwd_kernel(const NormBwdArgs a) {
@@ -429,23 +431,16 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
   dependent_launch();
   dependent_wait();
   const int cols = static_cast<int>(a.cols);
-  const int shift = ODD ? static_cast<int>(rt.first * a.cols & 7) : 0;
-  const int nvec = ODD ? (shift + cols + 7) / 8 : cols / 8;
-  // the row's elements of vector i: lo..hi - 1 (ODD)
-  const auto lo_of = [&](int i) { return i == 0 ? shift : 0; };
-  const auto hi_of = [&](int i) { return min(8, shift + cols - 8 * i); };
-  const auto whole = [&](int i) { return !ODD || (lo_of(i) == 0 && hi_of(i) == 8); };
-  const auto at_of = [&](int64_t row, int i) {   // a multiple of 8, at least 0
-    return row * a.cols - shift + 8 * i;
-  };
+  const RowVectors<ODD> vecs(a.rows, a.cols, rt.first);
+  const int nvec = vecs.count;
   const auto read = [&](Vec<DT, 8>& v, const void* p, int64_t row, int i) {
-    const T* q = static_cast<const T*>(p) + at_of(row, i);
-    if (ODD && i == nvec - 1 && row == a.rows - 1) load_head(v, q, hi_of(i));   // the tensor's end
+    const T* q = static_cast<const T*>(p) + vecs.at(row, i);
+    if (vecs.cut(row, i)) load_head(v, q, vecs.held(row, i));
     else v.load(q);
   };
   // The elements of other rows, as 0: once they are there, so that no load waits.
   const auto mask = [&](Vec<DT, 8>& v, int i) {
-    if (!whole(i)) v.keep(lo_of(i), hi_of(i));
+    if (!vecs.whole(i)) v.keep(vecs.lo(i), vecs.hi(i));
   };
   float gw[kShared ? 1 : NV][8];
   Vec<DT, 8> wv[NV], gv[NV], hv[NV];
@@ -490,7 +485,7 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
   }
   if constexpr (ODD)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) wv[j] = between<DT>(wv[j], wn[j], 8 - shift);
+    for (int j = 0; j < NV; ++j) wv[j] = between<DT>(wv[j], wn[j], 8 - vecs.shift);
   int par = 0;
   for (int64_t row = rt.first; row < a.rows; row += rt.step, par ^= 1) {
     Vec<DT, 8> gn[NV], hn[NV], rv[NV];
@@ -542,12 +537,12 @@ __global__ void __launch_bounds__(WARP || NV == 1 ? 256 : 512, NV == 1 ? 3 : WAR
         sh_gw[(2 * j + 1) * nt + tid] = make_float4(w[4], w[5], w[6], w[7]);
       }
       if (i < nvec) {
-        T* out = static_cast<T*>(a.gh) + at_of(row, i);
+        T* out = static_cast<T*>(a.gh) + vecs.at(row, i);
         Vec<DT, 8> ov;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ov.set2(e, o[2 * e], o[2 * e + 1]);
-        if (whole(i)) ov.store(out);
-        else store_part<DT>(out, ov, lo_of(i), hi_of(i));
+        if (vecs.whole(i)) ov.store(out);
+        else store_part<DT>(out, ov, vecs.lo(i), vecs.hi(i));
       }
       if (kAhead) {
         gv[j] = gn[j];

@@ -261,6 +261,23 @@ def test_norm_gradient_of_unaligned_tensors(mx, cuda, shape):
         check_gradient(mx, values(rows, cols, t, 61), values(rows, cols, t, 62), w, None)
 
 
+@pytest.mark.parametrize("shape", [(2, 1), (2, 2), (4, 3), (3, 5), (5, 3), (1, 7), (700, 1), (1300, 5)], ids=str)
+def test_norm_gradient_of_few_columns(mx, cuda, shape):
+    """Rows shorter than a vector of 8, several of which share the tensors' last,
+    incomplete one; tensors that end with their storage."""
+    rows, cols = shape
+    for t in (torch.bfloat16, torch.float16, torch.float32):
+        def at_end(seed):
+            held = torch.full((rows * cols + 8,), float("nan"), dtype=t, device=cuda)
+            return held[8:].view(rows, cols).copy_(values(rows, cols, t, seed))
+        g, h, gr = (at_end(71 + i) for i in range(3))
+        w = (1 + 0.2 * torch.randn(cols, generator=torch.Generator().manual_seed(5))).to(t).cuda()
+        check_gradient(mx, g, h, w, None)
+        gh, gw = check_gradient(mx, g, h, w, gr)
+        got = mx.rms_norm_bwd(g, h, w, eps=1e-5, grad_residual=gr, out=gr)
+        assert torch.equal(got[0], gh) and torch.equal(got[1], gw)
+
+
 @pytest.mark.parametrize("cols", [3, 131, 355, 1001, 2003, 9001])
 def test_norm_gradient_nan_stays_in_its_row(mx, cuda, cols):
     """Rows that share 16 bytes with one that holds NaN or Inf."""
