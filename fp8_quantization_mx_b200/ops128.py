@@ -424,7 +424,6 @@ class FP8NormLinear128(torch.autograd.Function):
         ctx.save_for_backward(*yt, *(wq[2:] if need_h else (None, None)), x if h is None else h,
                               norm_weight)
         ctx.eps, ctx.grad_format, ctx.weight_dtype = eps, grad_format, weight.dtype
-        ctx.has_residual = residual is not None
         # (without a residual h is x itself: a copy would be a second output)
         return gemm128(codes, scales, wq[0], wq[1]), h
 
@@ -438,7 +437,11 @@ class FP8NormLinear128(torch.autograd.Function):
             gx, gn = rms_norm_bwd(gy, h, norm_weight, ctx.eps,
                                   grad_residual=None if grad_h is None else grad_h.contiguous())
             gn = gn.to(norm_weight.dtype)
-        return gx, gx if ctx.has_residual else None, gn, gw, None, None
+        need_x, need_res = ctx.needs_input_grad[:2]
+        # one gradient for both, but in memory of its own for each: a leaf keeps the
+        # tensor that it is given and adds to it in place
+        gr = None if not need_res else gx.clone() if need_x else gx
+        return gx if need_x else None, gr, gn, gw, None, None
 
 
 def _layer_inputs(**tensors):

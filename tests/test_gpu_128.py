@@ -440,6 +440,21 @@ def test_norm_linear_forward_and_backward(mx, cuda, T, K, N):
         assert np.linalg.norm(f64(got) - want) <= 2 * 2.0 ** -4 * np.linalg.norm(want)
 
 
+def test_norm_linear_gradients_accumulate_apart(mx, cuda):
+    """Two backward passes into the same leaves of three dimensions: twice one
+    pass's gradient (exactly: a doubling), in memory of their own."""
+    x, r, nw, w = layer_inputs(60, 256, 136)
+    x, r = (t.view(4, 15, 256).requires_grad_() for t in (x, r))
+    nw.requires_grad_(), w.requires_grad_()
+    gy, gh = (torch.randn(4, 15, n, device=cuda).bfloat16() for n in (136, 256))
+    once = torch.autograd.grad(mx.rms_norm_linear128(x, nw, w, residual=r), (x, r, nw, w), (gy, gh))
+    for _ in range(2):
+        torch.autograd.backward(mx.rms_norm_linear128(x, nw, w, residual=r), (gy, gh))
+    for t, g in zip((x, r, nw, w), once):
+        assert torch.equal(t.grad, 2 * g)
+    assert x.grad.untyped_storage().data_ptr() != r.grad.untyped_storage().data_ptr()
+
+
 def test_linear_gradients_by_what_is_asked(mx, cuda):
     x, _, _, w = layer_inputs(70, 256, 136)
     gy = torch.randn(2, 35, 136, device=cuda).bfloat16()

@@ -1,0 +1,68 @@
+"""The tensor layer of the 128-element operators on a host without a GPU, with
+plain torch in the kernels' place."""
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def layers(mx, monkeypatch):
+    """ops128 with its operators in plain arithmetic, without FP8."""
+    from fp8_quantization_mx_b200 import ops128
+
+    def quantize128(x, *args, direction="rows", **kw):
+        return {"rows": (x, None), "cols": (x.t(), None), "both": (x, None, x.t(), None)}[direction]
+
+    def norm(x, weight, residual=None, eps=1e-6, return_y=False):
+        h = x if residual is None else x + residual
+        y = h * torch.rsqrt(h.square().mean(1, keepdim=True) + eps) * weight
+        return y, None, None if residual is None else h, y if return_y else None
+
+    def norm_bwd(gy, h, weight, eps, grad_residual=None):
+        r = torch.rsqrt(h.square().mean(1, keepdim=True) + eps)
+        n, g = h * r, gy * weight
+        gh = r * (g - n * (g * n).mean(1, keepdim=True))
+        return gh if grad_residual is None else gh + grad_residual, (gy * n).sum(0)
+
+    monkeypatch.setattr(ops128, "quantize128", quantize128)
+    monkeypatch.setattr(ops128, "rms_norm_quantize", norm)
+    monkeypatch.setattr(ops128, "rms_norm_bwd", norm_bwd)
+    monkeypatch.setattr(ops128, "gemm128", lambda a, sa, b, sb, **kw: a @ b.t())
+    monkeypatch.setattr(ops128, "_layer_inputs", lambda **kw: None)
+    return ops128
+
+
+def plain_layer(x, nw, w, r, eps=1e-6):
+    h = x if r is None else x + r
+    return h * torch.rsqrt(h.square().mean(-1, keepdim=True) + eps) * nw @ w.t(), h
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8)], ids=str)
+@pytest.mark.parametrize("asked", ["x residual", "x", "residual", "norm_weight", "weight",
+                                   "x residual norm_weight weight"])
+def test_gradients_of_x_and_residual_accumulate_apart(layers, shape, asked):
+    """Two backward passes into the same leaves: each gradient is the sum of
+    both, in memory of its own, and exists where it was asked for."""
+    g = torch.Generator().manual_seed(0)
+    names = ("x", "residual", "norm_weight", "weight")
+    sizes = (shape, shape, (8,), (4, 8))
+    made = [torch.randn(s, generator=g, dtype=torch.float64) for s in sizes]
+    mine, plain = ({n: t.clone().requires_grad_(n in asked.split()) for n, t in zip(names, made)}
+                   for _ in range(2))
+    for seed in (1, 2):
+        g.manual_seed(seed)
+        gy, gh = (torch.randn(*shape[:-1], n, generator=g, dtype=torch.float64) for n in (4, 8))
+        for t, out in ((mine, layers.rms_norm_linear128(mine["x"], mine["norm_weight"], mine["weight"],
+                                                        residual=mine["residual"])),
+                       (plain, plain_layer(plain["x"], plain["norm_weight"], plain["weight"],
+                                           plain["residual"]))):
+            both = [(o, d) for o, d in zip(out, (gy, gh)) if o.requires_grad]
+            torch.autograd.backward(*zip(*both))
+    for n in names:
+        a, b = mine[n].grad, plain[n].grad
+        assert (a is None) == (n not in asked.split()) == (b is None)
+        if a is not None:   # some 50 roundings of 2^-53 each, of values up to about 10
+            assert torch.allclose(a, b, rtol=0, atol=1e-12)
+    if mine["x"].grad is not None and mine["residual"].grad is not None:
+        assert mine["x"].grad.untyped_storage().data_ptr() != \
+            mine["residual"].grad.untyped_storage().data_ptr()
