@@ -35,7 +35,8 @@ def _on(device):
 
 # Calls with nothing unusual about them go through a C++ module that makes the
 # same checks, tensors and C calls (csrc/mx_fast128.cpp); it leaves every other
-# call to the code below. None until first used, False where it was not built.
+# call to the code below. None until first used, False where it was not built
+# (or for another torch or Python).
 _fast = None
 
 
@@ -44,7 +45,7 @@ def _bind_fast():
     lib = _c.load_library()
     try:
         from . import _fast128
-    except ModuleNotFoundError:
+    except ImportError:
         _fast = False
         return False
     _fast128.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -1,6 +1,8 @@
 """The tensor layer of the 128-element operators on a host without a GPU, with
 plain torch in the kernels' place."""
 
+import sys
+
 import pytest
 import torch
 
@@ -66,3 +68,18 @@ def test_gradients_of_x_and_residual_accumulate_apart(layers, shape, asked):
     if mine["x"].grad is not None and mine["residual"].grad is not None:
         assert mine["x"].grad.untyped_storage().data_ptr() != \
             mine["residual"].grad.untyped_storage().data_ptr()
+
+
+@pytest.mark.parametrize("there", [False, True], ids=["missing", "unloadable"])
+def test_calls_without_the_extension_module_are_left_to_python(mx, monkeypatch, tmp_path, there):
+    """The C++ module may not have been built, or for another torch."""
+    from fp8_quantization_mx_b200 import ops128
+    if there:
+        (tmp_path / "_fast128.so").write_bytes(b"not a library")
+    monkeypatch.setattr(mx, "__path__", [str(tmp_path)])
+    monkeypatch.delattr(mx, "_fast128", raising=False)
+    monkeypatch.delitem(sys.modules, "fp8_quantization_mx_b200._fast128", raising=False)
+    monkeypatch.setattr(ops128, "_fast", None)
+    assert ops128._bind_fast() is False and ops128._fast is False
+    with pytest.raises(ValueError, match="CUDA"):   # Python's own check
+        ops128.quantize128(torch.zeros(4, 256))
