@@ -15,6 +15,7 @@ import hashlib
 import os
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -99,8 +100,20 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     """Builds libmx.so unless the one in place was built from these exact
     sources and flags (its recorded source hash matches); file times are not
     trusted, so a stale library is always rebuilt. The torch binding's
-    extension module is kept up to date beside it."""
-    build_fast(force)
+    extension module is kept up to date beside it; where it cannot be built,
+    Python makes its calls."""
+    lib = build_library(force, verbose, extra)
+    try:
+        build_fast(force)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        if not isinstance(e, ImportError) and os.path.exists(FAST):
+            os.remove(FAST)   # it may be of another source, torch or Python
+        warnings.warn(f"{FAST} was not built, calls will take longer: {e}")
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, extra=None) -> str:
+    """build() without the extension module."""
     want = source_hash(extra)
     if not force and not verbose and os.path.exists(LIB) and _stamp() == want:
         return LIB

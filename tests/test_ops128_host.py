@@ -83,3 +83,24 @@ def test_calls_without_the_extension_module_are_left_to_python(mx, monkeypatch, 
     assert ops128._bind_fast() is False and ops128._fast is False
     with pytest.raises(ValueError, match="CUDA"):   # Python's own check
         ops128.quantize128(torch.zeros(4, 256))
+
+
+@pytest.mark.parametrize("why", ["no torch", "no compiler", "does not compile"])
+def test_the_library_builds_without_the_extension_module(mx, monkeypatch, tmp_path, why):
+    """The C library needs neither torch's headers nor a host compiler for them:
+    without the module, or with one that is out of date, there is a warning."""
+    from fp8_quantization_mx_b200 import build as b
+    fast = tmp_path / "_fast128.so"
+    fast.write_bytes(b"of another source")
+    monkeypatch.setattr(b, "FAST", str(fast))
+    if why == "no torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    elif why == "no compiler":
+        monkeypatch.setenv("PATH", str(tmp_path))
+    else:
+        (tmp_path / "broken.cpp").write_text("#error no such torch\n")
+        monkeypatch.setattr(b, "FAST_SRC", str(tmp_path / "broken.cpp"))
+    with pytest.warns(UserWarning, match="_fast128"):
+        assert b.build() == b.LIB
+    # what is out of date is not loaded (nothing is known of it without torch)
+    assert fast.exists() == (why == "no torch")
