@@ -41,8 +41,9 @@
 // pairs in halves 443; a shorter loop 431.
 //
 // Every wait is bounded in time (mbar_wait): one that runs out sets the
-// caller's status word, and the CTA drains its copies and MMAs, frees its TMEM
-// and returns.
+// caller's status word, and the CTA stores NaN for the sums that it could not
+// make, in this tile and its further ones, drains its copies and MMAs, frees its
+// TMEM and returns.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -626,14 +627,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int col_scale = C::kRowSlot / 4 + part * C::kCols;
     const uint32_t done0 = sm.done(h, 0);
     bool ok = true;
-    for (int64_t t = t_first; ok && t < ntiles; t += t_step) {
+    const float none = __int_as_float(0x7fc00000);   // for sums left unmade
+    for (int64_t t = t_first; t < ntiles; t += t_step) {
       int64_t p, q;
       tile_at(t, tiles_p, tiles_q, p, q);
       const int64_t p0 = p * C::kTileRows + row_rank * kRows, q0 = q * C::BN;
       float acc[C::kCols];
 #pragma unroll
-      for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
-      for (int kb = kb0; kb < kb1; kb += C::kBatch, ++nslot) {
+      for (int i = 0; i < C::kCols; ++i) acc[i] = ok ? 0.0f : none;
+      for (int kb = ok ? kb0 : kb1; kb < kb1; kb += C::kBatch, ++nslot) {
         ok &= tc::mbar_wait(sm.sfull(nslot & 1), (nslot >> 1) & 1, sm.abort_flag, g.status, kStatusSums);
         const float* slot = sm.scl_ptr + (nslot & 1) * (C::kSlot / 4);
         // (not unrolled: the loop's length in instructions is what the issuing
@@ -642,11 +644,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll 1
         for (int at = 0; at < C::kBatch; ++at) {
           if (kb + at >= kb1) break;
-          const float s = slot[row_scale + at * C::kRowSets * kRows];
-          // (after a wait that ran out the loop goes on, every later wait returns
-          // at once, and nothing is stored: tcgen05.ld needs the whole warp)
+          float s = slot[row_scale + at * C::kRowSets * kRows];
+          // (after a wait that ran out the loop goes on to the tile's end and every
+          // later wait returns at once, since tcgen05.ld needs the whole warp)
           ok &= tc::mbar_wait(done0 + 8 * (n & (C::S - 1)), (n / C::S) & 1, sm.abort_flag, g.status,
                               kStatusSums);
+          if constexpr (!C::PAIR)   // (pairs: after the loop; here it cost them 2.5%, there others 4%)
+            if (!ok) s = none;
           __syncwarp();
           tc::tc_fence_after();
           const uint32_t b = n & (C::NBUF - 1);
@@ -703,11 +707,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (!__all_sync(~0u, ok)) {
         ok = false;
-        break;
+        if constexpr (C::PAIR)
+#pragma unroll
+          for (int i = 0; i < C::kCols; ++i) acc[i] = none;
       }
       if (!C::PAIR && g.split > 1) {
         // the ring is idle: every K-block loaded has been multiplied. (The
-        // generic writes below follow the MMAs' reads through `done`.)
+        // generic writes below follow the MMAs' reads through `done`.) Where not,
+        // see below.
 #pragma unroll
         for (int i = 0; i < C::kCols; i += 4) {
           const float4 v = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
@@ -735,6 +742,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (g.split > 1) {
       int64_t p, q;
       tile_at(t_first, tiles_p, tiles_q, p, q);
+      if (!ok)   // once more: copies may have landed on it since
+#pragma unroll 1
+        for (int c = part * C::kCols; c < (part + 1) * C::kCols; ++c)
+          *reinterpret_cast<float*>(sm.ring_ptr + (C::SWAP ? part_at<kRows>(c, quarter * 32 + lane)
+                                                           : part_at<C::BN>(quarter * 32 + lane, c))) = none;
       tc::cluster_sync();   // every partial tile is in shared memory
       if (g.split == 2) add_split<C, 2>(sm, g, p * kRows, q * C::BN, rank);
       else if (g.split == 4) add_split<C, 4>(sm, g, p * kRows, q * C::BN, rank);

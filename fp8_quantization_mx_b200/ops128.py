@@ -328,7 +328,9 @@ def gemm128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor
     """D [M, N] = A B^T on the tensor cores: A [M, K] with tile scales, B [N, K]
     with tile or block scales (by the shape of ``b_scales``). bf16 or float32
     out; ``status``: an optional int32 device tensor set nonzero if one of the
-    kernel's waits timed out."""
+    kernel's waits timed out (after a second, which nothing but a device held up
+    from outside takes). What of D was left unmade then is NaN, with or without a
+    status."""
     _fp8_format(a_format, "a_format")
     _fp8_format(b_format, "b_format")
     if out_dtype not in (torch.bfloat16, torch.float32):

@@ -370,8 +370,9 @@ int mx_rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const
  * D is row-major [M, N], bf16 (nearest even) or float (out_fp32 = 1). The
  * forward and input-gradient products of a linear layer take block-scaled
  * weights; its weight gradient two column-quantized operands. M, N, K are
- * free; K == 0 writes zeros. status as in mx_gemm. Results do not vary from
- * run to run on one GPU model. */
+ * free; K == 0 writes zeros. status as in mx_gemm; where a wait timed out, the
+ * values of D that were left unmade are NaN, so that a call without a status
+ * shows it too. Results do not vary from run to run on one GPU model. */
 int mx_gemm128(const void* a_codes, int64_t lda, const float* a_scales, int64_t ldsa, int a_format,
                const void* b_codes, int64_t ldb, const float* b_scales, int64_t ldsb, int b_format,
                int b_flags, int64_t M, int64_t N, int64_t K, int out_fp32, void* d, int* status,
