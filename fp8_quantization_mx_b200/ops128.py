@@ -326,7 +326,8 @@ def gemm128(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor
             b_scales: torch.Tensor, a_format: int = E4M3, b_format: int = E4M3,
             out_dtype=torch.bfloat16, out=None, status=None):
     """D [M, N] = A B^T on the tensor cores: A [M, K] with tile scales, B [N, K]
-    with tile or block scales (by the shape of ``b_scales``). bf16 or float32
+    with tile or block scales (by the shape of ``b_scales``). The product of a
+    K-block's two scales has to lie in float32's normal range. bf16 or float32
     out; ``status``: an optional int32 device tensor set nonzero if one of the
     kernel's waits timed out (after a second, which nothing but a device held up
     from outside takes). What of D was left unmade then is NaN, with or without a

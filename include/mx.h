@@ -366,8 +366,10 @@ int mx_rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const
 /* D[M, N] = A . B^T of two such operands on the tensor cores: A [M, K] with
  * tile scales, B [N, K] with tile scales or (b_flags = MX_BLOCK128) block
  * scales. Each K-block of 128 is multiplied with fp32 accumulation
- * (tcgen05.mma.kind::f8f6f4) and added, times its two scales, to a float sum;
- * D is row-major [M, N], bf16 (nearest even) or float (out_fp32 = 1). The
+ * (tcgen05.mma.kind::f8f6f4) and added to a float sum, times the product of its
+ * two scales, which is rounded to float first: a product below 2^-126 has fewer
+ * bits (below 2^-150 it is 0), one of 2^128 or more is infinite, also where the
+ * K-block's sum would bring the result back into range. D is row-major [M, N], bf16 (nearest even) or float (out_fp32 = 1). The
  * forward and input-gradient products of a linear layer take block-scaled
  * weights; its weight gradient two column-quantized operands. M, N, K are
  * free; K == 0 writes zeros. status as in mx_gemm; where a wait timed out, the

@@ -378,6 +378,31 @@ def test_gemm_of_integers_is_exact(mx, cuda, shape, block):
     assert np.array_equal(f64(d), av @ bv.T)
 
 
+@pytest.mark.parametrize("shape", [(8, 136), (300, 520)], ids=str)
+@pytest.mark.parametrize("block", [True, False])
+def test_gemm_scale_products_round_to_float(mx, cuda, shape, block):
+    """One K-block of small integers, whose sum is exact, under scales from 2^-126
+    to 2^100: every value is that sum times the scales' product rounded to float
+    (2^-126 and more: its own rounding alone), rounded once."""
+    M, N = shape
+    K = 128
+    rng = np.random.default_rng(9)
+    a, b = (rng.integers(-8, 9, (n, K)).astype(np.float64) for n in (M, N))
+    sa = np.float32(rng.uniform(1, 2, M) * 2.0 ** rng.integers(-126, 101, M))
+    sb = np.float32(rng.uniform(1, 2, N) * 2.0 ** rng.integers(-126, 101, N))
+    if block:
+        sb = np.repeat(np.float32([1.7 * 2.0 ** 90, 1.3 * 2.0 ** -80, 1.1 * 2.0 ** -20] * 2), 128)[:N]
+    scales = [torch.from_numpy(sa).cuda().view(M, 1),
+              torch.from_numpy(sb[::128].copy() if block else sb).cuda().view(-1, 1)]
+    codes = [torch.from_numpy(P.encode(v, E4M3)).cuda() for v in (a, b)]
+    d = mx.gemm128(codes[0], scales[0], codes[1], scales[1], out_dtype=torch.float32).cpu().numpy()
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        p = sa[:, None] * sb[None]
+        want = np.float32(p.astype(np.float64) * (a @ b.T))
+    assert p.dtype == np.float32 and np.any((p < 2.0 ** -126) & (p > 0)) and np.isinf(p).any()
+    assert np.array_equal(d, want, equal_nan=True)
+
+
 def test_gemm_nan_scale_reaches_its_row_alone(mx, cuda):
     for M in (8, 300):
         x = torch.randn(M, 512, device=cuda)
