@@ -461,6 +461,7 @@ def linear128(x: torch.Tensor, weight: torch.Tensor, grad_format: int = E4M3) ->
     ``FP8Linear128``). x bfloat16 [..., K], weight bfloat16 [N, K];
     ``grad_format``: the output gradient's FP8 format."""
     _layer_inputs(x=x, weight=weight)
+    _fp8_format(grad_format, "grad_format")
     if not torch.is_grad_enabled():   # nothing is kept for a backward pass
         x, weight = x.detach(), weight.detach()
     y = FP8Linear128.apply(x.reshape(-1, x.shape[-1]), weight, grad_format)
@@ -474,6 +475,7 @@ def rms_norm_linear128(x: torch.Tensor, norm_weight: torch.Tensor, weight: torch
     ``linear128``."""
     _layer_inputs(x=x, norm_weight=norm_weight, weight=weight,
                   **({} if residual is None else {"residual": residual}))
+    _fp8_format(grad_format, "grad_format")
     shape = x.shape
     if residual is not None and residual.shape != shape:
         raise ValueError(f"residual must be {list(shape)}, got {list(residual.shape)}")

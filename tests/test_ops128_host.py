@@ -70,6 +70,17 @@ def test_gradients_of_x_and_residual_accumulate_apart(layers, shape, asked):
             mine["residual"].grad.untyped_storage().data_ptr()
 
 
+def test_layers_refuse_a_gradient_format_before_the_forward_pass(layers):
+    x, nw, w = torch.ones(3, 8, requires_grad=True), torch.ones(8), torch.ones(4, 8)
+    for fmt in (0, 3, -1, None):
+        with pytest.raises(ValueError, match="grad_format"):
+            layers.linear128(x, w, grad_format=fmt)
+        with pytest.raises(ValueError, match="grad_format"):
+            layers.rms_norm_linear128(x, nw, w, grad_format=fmt)
+    for fmt in (layers.E4M3, layers.E5M2):
+        layers.linear128(x, w, grad_format=fmt).sum().backward()
+
+
 @pytest.mark.parametrize("there", [False, True], ids=["missing", "unloadable"])
 def test_calls_without_the_extension_module_are_left_to_python(mx, monkeypatch, tmp_path, there):
     """The C++ module may not have been built, or for another torch."""
