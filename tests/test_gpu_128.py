@@ -183,6 +183,22 @@ def test_norm_equals_the_definition(mx, cuda, shape):
             assert h is None
 
 
+@pytest.mark.parametrize("shape", [(450, 4104), (700, 5120), (320, 6144), (500, 7168), (310, 8184), (500, 1016),
+                                   (3000, 1024)], ids=str)
+def test_norm_and_gradient_of_wide_rows(mx, cuda, shape):
+    """More rows than CTAs at every spread of a wide row over threads."""
+    rows, cols = shape
+    for i, t in enumerate((torch.bfloat16, torch.float32)):
+        x, r, g = (values(rows, cols, t, 77 + 10 * i + j) for j in range(3))
+        w = (1 + 0.2 * torch.randn(cols, generator=torch.Generator().manual_seed(i))).to(t).cuda()
+        codes, scales, h, _ = mx.rms_norm_quantize(x, w, r, eps=1e-5)
+        h64, y64 = P.norm(f64(x), f64(r), f64(w), float(np.float32(1e-5)))
+        check_codes(codes, scales, y64, E4M3, False)
+        # one float addition and one rounding
+        assert np.all(np.abs(f64(h) - h64) <= (half_step(t) + U32) * np.abs(h64) + torch.finfo(t).tiny)
+        check_gradient(mx, g, x, w, r)
+
+
 def test_norm_in_place_and_zero_rows(mx, cuda):
     x, r = values(9, 512, torch.bfloat16, 1), values(9, 512, torch.bfloat16, 2)
     x[4], r[4] = 0, 0
@@ -413,6 +429,38 @@ def test_gemm_nan_scale_reaches_its_row_alone(mx, cuda):
         assert bad.nonzero().flatten().tolist() == [5] and bool(torch.isfinite(d[:5]).all())
 
 
+@pytest.mark.parametrize("rows", [(0, 5, 0, 130), (128, 300, 256, 200), (256, 700, 128, 600)], ids=str)
+def test_gemm_of_slices_of_larger_operands(mx, cuda, rows):
+    """Rows and K-blocks of larger codes and scales give what copies of them give:
+    pitches beyond the least, and other codes behind a row's end."""
+    a0, M, b0, N = rows
+    a = mx.quantize128(torch.randn(1000, 1280, device=cuda))
+    b = mx.quantize128(torch.randn(900, 1280, device=cuda))
+    bb = mx.quantize128(torch.randn(900, 1280, device=cuda), block=True)
+
+    def copied(codes, scales, block):
+        n, k = codes.shape
+        held = torch.full((n, (k + 15) // 16 * 16), 0x7F, dtype=torch.uint8, device=cuda)
+        held[:, :k] = codes
+        if block:
+            return held[:, :k], scales.clone()
+        laid = torch.full((scales.shape[1], (n + 3) // 4 * 4), float("nan"), device=cuda)
+        laid[:, :n] = scales.t()
+        return held[:, :k], laid.t()[:n]
+
+    for k0, k1 in ((0, 1280), (256, 1280), (128, 901)):
+        t0, t1 = k0 // 128, (k1 + 127) // 128
+        sa = a[0][a0:a0 + M, k0:k1], a[1][a0:a0 + M, t0:t1]
+        sides = [(b[0][b0:b0 + N, k0:k1], b[1][b0:b0 + N, t0:t1], False)]
+        if k0 == 0:
+            blocks = bb[1][b0 // 128:(b0 + N + 127) // 128, :t1]
+            sides.append((bb[0][b0:b0 + N, :k1], blocks, True))
+        for cb, scb, block in sides:
+            got = mx.gemm128(*sa, cb, scb)
+            assert torch.isfinite(got).all()
+            assert torch.equal(got, mx.gemm128(*copied(*sa, False), *copied(cb, scb, block)))
+
+
 def test_gemm_empty(mx, cuda):
     a = mx.quantize128(torch.randn(5, 256, device=cuda))
     none = torch.empty(0, 256, dtype=torch.uint8, device=cuda)
@@ -536,6 +584,37 @@ def test_layer_in_a_graph_and_on_another_stream(mx, cuda):
     side.synchronize()
     want = step(x, r)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_training_step_in_a_graph(mx, cuda):
+    """Both layers' forward and backward pass captured once; replays on new inputs
+    give what eager passes give."""
+    x, r, nw, w = layer_inputs(96, 512, 512)
+    leaves = [t.clone().requires_grad_() for t in (x, r, nw, w)]
+    gy = torch.randn(96, 512, device=cuda).bfloat16()
+
+    def step(lx, lr, lnw, lw):
+        y, h = mx.rms_norm_linear128(lx, lnw, lw, residual=lr)
+        z = mx.linear128(y, lw, grad_format=E5M2)
+        return torch.autograd.grad([z, h], [lx, lr, lnw, lw], [gy, gy])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*leaves)
+    for seed in (0, 3):
+        new = layer_inputs(96, 512, 512, seed)
+        with torch.no_grad():
+            for t, n in zip(leaves, new):
+                t.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step(*(n.requires_grad_() for n in new))):
+            assert torch.equal(a, b)
 
 
 def test_norm_gradient_in_a_graph(mx, cuda):
