@@ -4,7 +4,9 @@
 // tokens' GEMM for 4). Each function returns None for any call that it does not
 // take (another device than the current one, a tensor subclass, an argument
 // that is refused, an empty tensor): Python then makes the call, or raises. A
-// status other than MX_OK comes back as an int.
+// status other than MX_OK comes back as an int. The outputs come from torch's
+// CUDA allocator past its dispatcher: dispatch modes do not see them made, and
+// torch.utils.deterministic does not fill them.
 
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -31,14 +31,17 @@
 // What bounds it. One K-block of a pair's tile is 512 clocks of MMA; with
 // nothing but the loads and MMAs it took 344 ns at the clock that the power
 // limit left (3.6 PFLOP/s), as a whole 382 ns with block scales and 570 with
-// column scales, whose second multiplication fills the FMA pipe for as long as
-// the MMAs run. 8192^3 takes 431 us (2.55 PFLOP/s) in bursts and 516 us in a
-// steady loop at 1.37 GHz and 990 W; a library product of the same codes with
-// one scale for the whole tensor, 418 us at 1.31 GHz. Few tokens are bound by
-// the weights' bytes and 3 to 4 us of start and end: 1 x 8192 x 8192 14.4 us
-// (4.7 TB/s), 16 x 1536 x 2048 4.2 us. What each step gave (8192^3, us): one CTA
-// per tile 673; issuing and scale-loading warps of their own, packed sums 457;
-// pairs in halves 443; a shorter loop 431.
+// column scales. There no pipe is full (4096 x 4096 x 16384: FMA pipe 52%, tensor
+// pipe 49%, issue 53%): an accumulating warp waits, loads, multiplies row by
+// column scale, adds and releases, and this chain overlaps only in part with the
+// next K-block's MMAs. 8192^3 takes 443 us (2.48 PFLOP/s) in bursts and 501 to
+// 529 us, by the card, in a steady loop at the power limit (1.37 GHz at 990 W); a
+// library product of the same codes with one scale for the whole tensor, 418 us
+// at 1.31 GHz. Few tokens are bound by the weights' bytes and 4 us of start and
+// end: 1 x 8192 x 8192 14.1 us (4.8 TB/s), 16 x 1536 x 2048 4.7 us. What each step
+// gave (8192^3, us): one CTA per tile 673; issuing and scale-loading warps of
+// their own, packed sums 457; pairs in halves 443; a shorter loop 431; NaN for
+// sums left unmade 443 (438 without it on the same card).
 //
 // Every wait is bounded in time (mbar_wait): one that runs out sets the
 // caller's status word, and the CTA stores NaN for the sums that it could not
@@ -855,7 +858,7 @@ cudaError_t launch(const Gemm128& u, const Gemm128Args& g, int dev, int sms, cud
 // of a CTA times a K-block's time, a start and end, and what joining a split
 // costs (more for wide tiles, whose partial sums cross the cluster). Its figures
 // (us) are fitted to measurements of every cut at 120 sizes, of which it chose
-// the best or one 1% slower on average, 14% at worst (2048 x 511 x 6000):
+// the best or one 1% slower on average, 15% at worst (2048 x 511 x 6000):
 //   a tile that is finer than needed loses to its number of waves, one that is
 //   coarser leaves SMs idle: 128 x 8192 x 4096 takes 10.6 us in 64-wide tiles,
 //   13.1 in 128-wide ones on two CTAs each, 18 in pairs' tiles; 512 x 8192 x
@@ -982,8 +985,8 @@ Gemm128 part_of(const Gemm128& u, int64_t m0, int64_t M, int64_t n0, int64_t N) 
 
 // Sizes a little over a multiple of 256 cost whole tiles, at times a whole wave
 // of them: rows and columns past the multiple are then products of their own,
-// if by the model that is cheaper (4099 x 2056 x 8192: one wave of three, 81 ->
-// 70 us). A further launch on the stream costs 1.7 us beyond its own time.
+// if by the model that is cheaper (4099 x 2056 x 8192: one wave of three, 84.5
+// -> 72.2 us). A further launch on the stream costs 1.7 us beyond its own time.
 cudaError_t launch_gemm128(const Gemm128& u, const Plan128* plan, cudaStream_t st) {
   constexpr double kLaunch = 1.7;
   int dev = 0, sms = 0, c4 = 0, c8 = 0;

@@ -408,14 +408,15 @@ __device__ __forceinline__ void store_part(typename Elem<DT>::T* p, Vec<DT, 8> v
 // A thread keeps its columns' share of gw in registers (shared memory with four
 // vectors a thread in a CTA) over all its rows; WARP: the CTA's eight warps add
 // theirs up at the end. (With four vectors a thread the next row's loads do not
-// fit the registers and wait.)
+// fit the registers and wait; they spill 120 to 192 bytes a thread in a CTA, the
+// forward pass 16 and, of floats, 236; fewer vectors up to 88.)
 //
 // ODD: the columns are no multiple of 8, so that rows start at any element of a
 // vector of the memory (mx_rowvec.h). A row's first and last vector hold elements
 // of its neighbours, which are masked: in place, another CTA may be writing those
 // meanwhile. Reads stop at the matrix's end. A thread takes rows a multiple of 8
 // apart (the launch sees to that), whose shifts are the same, and so keeps its
-// columns. (4097 x 3001: 25.9 us, 85 with an element at a time; 4 x 6940 5.6 us
+// columns. (4097 x 3001: 26.2 us, 85 with an element at a time; 4 x 6940 5.6 us
 // for 7.7; 5324 x 355 11.2 for 14.1. Loads that a branch had to wait for cost
 // 0.7 us each.)
 template <int DT, int NV, bool WARP, bool ODD>
@@ -715,9 +716,11 @@ Shape shape_of(int64_t nvec, int64_t rows, int sms) {
   return {false, nv, static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)};
 }
 
-// CTAs for `rows` rows with at most `threads` threads on an SM (what the
-// registers of the kernels' launch bounds allow: more CTAs than the SMs hold
-// would run as a second wave).
+// CTAs for `rows` rows with at most `threads` threads on an SM: what the
+// registers of the kernels' launch bounds allow. Some compiled kernels need more
+// than that, and half of their CTAs run as a second wave: the forward pass of
+// 4104 to 5632 columns (120 registers, two CTAs of 288 to 352 threads asked for,
+// one fits), of 520 to 1024 (192) and of floats of 264 to 512 (136).
 int64_t grid_for(const Shape& s, int64_t rows, int sms, int threads) {
   const int per_sm = threads / static_cast<int>(s.nt);
   const int64_t most = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);

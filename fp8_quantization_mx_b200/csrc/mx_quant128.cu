@@ -102,7 +102,8 @@ __device__ __forceinline__ void encode_cols(const Vec<DT, 16> (&v)[4], const flo
 // CTAs per SM that the registers are cut for. What hides a piece's load, sums
 // and stores is other CTAs: 32768 x 4096 both ways took 148, 123, 110, 110 us
 // with 2 to 5 of them (before the scales were shared out over the lanes: 103
-// with 4); floats spill beyond 3. One CTA that loads the next piece ahead, at 2
+// with 4). Floats, twice the registers of x, spill 8 to 32 bytes a thread with 3.
+// One CTA that loads the next piece ahead, at 2
 // per SM: 152 us.
 template <int DT>
 constexpr int ctas_per_sm() {
