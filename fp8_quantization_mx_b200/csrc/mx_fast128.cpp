@@ -43,11 +43,12 @@ constexpr int kBlock128 = 1 << 10, kPow2 = 1 << 11;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// A plain CUDA tensor on the current device (dev: found, or -1 to begin with).
+// A plain CUDA tensor on the current device (dev: found, or -1 to begin with),
+// whose memory holds its values.
 const at::Tensor* tensor(PyObject* o, int& dev) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || t.layout() != at::kStrided) return nullptr;
+  if (!t.is_cuda() || t.layout() != at::kStrided || t.is_neg()) return nullptr;
   const int d = t.get_device();
   if (dev < 0) {
     if (d != c10::cuda::current_device()) return nullptr;

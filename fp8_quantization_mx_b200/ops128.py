@@ -78,6 +78,12 @@ def _fp8_format(format, name="format"):
         raise ValueError(f"{name} must be E4M3 or E5M2")
 
 
+def _stored(t, name: str):
+    """Refuses a view that torch negates where it reads it: kernels read memory."""
+    if t.is_neg():
+        raise ValueError(f"{name} must not be lazily negated (use its resolve_neg())")
+
+
 def _matrix(t, name: str, device=None, dtype=None, shape=None):
     """Checks a 2-D CUDA tensor of a floating type whose rows are contiguous;
     returns its row pitch in elements."""
@@ -100,6 +106,7 @@ def _matrix(t, name: str, device=None, dtype=None, shape=None):
         raise ValueError(f"{name} must have contiguous rows")
     if rows > 1 and t.stride(0) < cols:
         raise ValueError(f"{name} must not have overlapping rows")
+    _stored(t, name)
     return t.stride(0) if rows > 1 else cols
 
 
@@ -112,6 +119,7 @@ def _contiguous(t, name: str, device, dtype, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    _stored(t, name)
 
 
 def _new_codes(rows: int, cols: int, device):
@@ -172,6 +180,7 @@ def _scales(t, name: str, device, rows: int, cols: int, block: bool) -> int:
     shape = ((rows + 127) // 128 if block else rows, nb)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    _stored(t, name)
     if block:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")

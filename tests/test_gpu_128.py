@@ -699,6 +699,24 @@ def test_tensor_layer_refuses(mx, cuda):
             call()
 
 
+def test_lazily_negated_tensors_are_refused(mx, cuda):
+    """The imaginary part of a conjugate is a view of the positive values that
+    torch negates where it reads them; the kernels would not."""
+    x = torch.randn(5, 1, dtype=torch.complex64, device=cuda).conj().imag
+    plain, w = x.resolve_neg(), torch.ones(1, device=cuda)
+    assert x.is_neg() and torch.equal(x, plain) and not plain.is_neg()
+    one = torch._neg_view(torch.ones(1, 1, device=cuda))
+    for call in (lambda: mx.quantize128(x), lambda: mx.rms_norm_quantize(x, w),
+                 lambda: mx.rms_norm_quantize(plain[:1], w, one), lambda: mx.rms_norm_bwd(one, one, w),
+                 lambda: mx.rms_norm_bwd(one.resolve_neg(), one.resolve_neg(), w, grad_residual=one)):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            call()
+    codes, scales = mx.quantize128(one.resolve_neg())
+    with pytest.raises(ValueError, match="resolve_neg"):
+        mx.gemm128(codes, torch._neg_view(scales), codes, scales)
+    assert torch.equal(mx.quantize128(plain)[0] >> 7, (plain < 0).byte())
+
+
 def test_layers_without_tokens_and_of_one_dimension(mx, cuda):
     _, _, nw, w = layer_inputs(1, 256, 136)
     w.requires_grad_()
